@@ -207,8 +207,10 @@ def prepare(case, seed):
         s["scale"] = 1.0 / n
         s["grad"] = TYPES[case["grad"]] if op == "grad" else None
         if own:
-            from logit_kl_divergence_b200 import KLDStats
+            from logit_kl_divergence_b200 import KLDStats, PackedLogits
             s["handle"] = KLDStats(n)
+            s["base"] = PackedLogits(s["codes"], s["heads"], v)
+            s["other"] = PackedLogits(*s["quant"], v) if both else s["quant"]
         return s
     groups, beams = case["groups"], case["beams"]
     if op == "select":
@@ -234,6 +236,8 @@ def prepare(case, seed):
     if own:
         from logit_kl_divergence_b200 import BeamSearch
         s["handle"] = BeamSearch(groups, beams)
+        if op == "reorder":
+            s["bound"] = s["handle"].bind([(x, 2) for x in s["states"]] + [(s["tokens"], 1)])
     return s
 
 
@@ -306,25 +310,23 @@ def run(state):
 
 
 def _own(state, op):
-    from logit_kl_divergence_b200 import PackedLogits, pack_logits
     if op == "pack":
+        from logit_kl_divergence_b200 import pack_logits
         return pack_logits(state["x"]).unpack(torch.float32)
+    h = state["handle"]
     if op in ("score", "grad"):
-        base = PackedLogits(state["codes"], state["heads"], state["v"])
-        q = state["quant"]
-        q = PackedLogits(*q, state["v"]) if isinstance(q, tuple) else q
+        base, quant = state["base"], state["other"]
         if op == "score":
-            rows = state["handle"].run_packed(base, q, state["tokens"], per_row=True)
+            rows = h.run_packed(base, quant, state["tokens"], per_row=True)
         else:
-            grad, rows = state["handle"].run_grad_packed(base, q, state["tokens"], scale=state["scale"],
-                                                         grad_dtype=state["grad"], per_row=True)
+            grad, rows = h.run_grad_packed(base, quant, state["tokens"], scale=state["scale"],
+                                           grad_dtype=state["grad"], per_row=True)
             rows["grad"] = grad
         rows["kld"], rows["nll"] = rows["kld"].float(), rows["nll"].float()
         return rows
     if op == "select":
-        return state["handle"].select(state["logits"], state["scores"], state["k"], finished=state["done"], eos=EOS)
-    states = [(x, 2) for x in state["states"]] + [(state["tokens"], 1)]
-    state["handle"].reorder(states, state["parents"], lengths=state["lengths"])
+        return h.select(state["logits"], state["scores"], state["k"], finished=state["done"], eos=EOS)
+    h.reorder(state["bound"], state["parents"], lengths=state["lengths"])
     return state["states"] + [state["tokens"]]
 
 
