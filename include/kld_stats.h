@@ -39,6 +39,8 @@
  *     excluded) surface in kld_stats_result().
  *   - A handle is bound to one device and is not thread-safe; use one handle
  *     per concurrent stream.
+ *   - KLD_ABI_VERSION counts changes to declarations that exist; functions
+ *     and types added beside them leave it.
  *
  * Row policy (the pages are silent; both this library and its test oracle
  * follow it):
@@ -378,6 +380,173 @@ kld_status_t kld_stats_run_static(const void* base, const void* quant,
                                   const int32_t* token_ids, int64_t N,
                                   int64_t V, kld_dtype_t dtype,
                                   kld_result_t* result_dev, void* stream);
+
+/* ======================================================================
+ * 8-bit logit checkpoints: logits kept for later passes (the base model's
+ * rows across the steps of a tuning run; the quant rows of a deferred
+ * backward pass) at 1 + 1/32 bytes an entry, with the statistic and the
+ * gradient read straight from them.
+ * ====================================================================== */
+
+/*
+ * Format of a checkpoint of [N, V] logits, nb = ceil(V / KLD_PACK_BLOCK):
+ *   codes  N * nb * KLD_PACK_BLOCK bytes, row-major, 16-byte aligned;
+ *   heads  N * nb uint32, row-major: one header per block of 128 columns.
+ * A block's entries are whole multiples of a power of two 2^e:
+ *   n_j = rint(x_j / 2^e) (ties to even), base = min_j n_j - 1,
+ *   code_j = n_j - base (1..255), code 0 = -inf (also the padding past V),
+ *   value_j = (base + code_j) * 2^e, an fp32 number, |value_j - x_j| <= 2^(e-1),
+ * with e the smallest integer >= max(floor(log2 max|x|) - 20, -126) for which
+ * max_j n_j - min_j n_j <= 254 (extremes over the entries above -inf);
+ *   head = base << 9 | (some code is 0) << 8 | (e + 128).
+ * No rounded quantity decides a code, so every implementation gives the same
+ * bits. A block without an entry above -inf has head 256. A block holding
+ * NaN, +inf or a magnitude of 2^126 or more has head 511 and reads as NaN:
+ * its row is NONFINITE to the statistic. With logits spanning R in a block the
+ * error is at most R / 254 either way.
+ */
+#define KLD_PACK_BLOCK 128
+typedef struct {
+  uint8_t* codes;
+  uint32_t* heads;
+} kld_packed_t;
+
+/*
+ * Write the checkpoint of [N, V] logits (device, contiguous, `dtype`, aligned
+ * to the element size) into out->codes / out->heads (caller-owned DEVICE
+ * memory of the sizes above). `device` is the device that holds them.
+ * Asynchronous on `stream`; allocates nothing. KLD_ERR_INVALID_ARG for NULL
+ * or misaligned pointers or sizes out of range, KLD_ERR_DTYPE.
+ */
+kld_status_t kld_pack_logits(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+                             const kld_packed_t* out, int device, void* stream);
+
+/*
+ * Restore the values of a checkpoint into [N, V] `out` (device, contiguous),
+ * exact in KLD_F32, rounded to nearest in the 16-bit types. Errors as
+ * kld_pack_logits.
+ */
+kld_status_t kld_unpack_logits(const kld_packed_t* packed, int64_t N, int64_t V, void* out,
+                               kld_dtype_t dtype, int device, void* stream);
+
+/* Optional per-row outputs of the packed calls: caller-owned DEVICE arrays of
+ * N values (kld_stats_rows' fields), each may be NULL. */
+typedef struct {
+  double* kld;
+  double* nll;
+  int32_t* amax_b;
+  int32_t* amax_q;
+} kld_fields_t;
+
+/*
+ * kld_stats_run with the base rows read from a checkpoint. The quant rows are
+ * dense (`quant`, `quant_dtype`, quant_packed NULL; no alignment tie to the
+ * base rows) or from a checkpoint of their own (quant_packed set, quant
+ * ignored). The statistics, flags and records are those of the restored
+ * values. fields may be NULL. Asynchronous on `stream`; read with
+ * kld_stats_result / kld_stats_rows / kld_stats_records.
+ */
+kld_status_t kld_stats_run_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
+                                  kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,
+                                  const int32_t* token_ids, int64_t N, int64_t V,
+                                  const kld_fields_t* fields, void* stream);
+
+/*
+ * kld_stats_run_grad with the base rows (and the quant rows, when
+ * quant_packed is set) read from checkpoints: the same statistic plus
+ *   grad[i][j] = scale * (softmax(q_i)_j - softmax(b_i)_j)
+ * of the restored values, zero on excluded rows, in one kernel that reads
+ * the rows once. grad: caller-owned DEVICE memory, [N, V] of grad_dtype,
+ * aligned to its element size. A non-finite scale is KLD_ERR_INVALID_ARG.
+ */
+kld_status_t kld_stats_run_grad_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
+                                       kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,
+                                       const int32_t* token_ids, int64_t N, int64_t V, void* grad,
+                                       kld_dtype_t grad_dtype, double scale,
+                                       const kld_fields_t* fields, void* stream);
+
+/* ======================================================================
+ * Beam search over logit rows: selection and the reordering of states.
+ * ====================================================================== */
+
+#define KLD_BEAM_MAX_BEAMS 64
+#define KLD_BEAM_MAX_K 128
+
+typedef struct kld_beam_s* kld_beam_t;
+
+/*
+ * A handle for up to max_groups groups (prompts) of max_beams beams, keeping
+ * up to max_k candidates a group (1 <= max_beams <= 64, 1 <= max_k <= 128).
+ * Owns a device workspace (about 30 KB + 1 KB per row and candidate set),
+ * released by kld_beam_destroy. Bound to one device, not thread-safe; calls
+ * whose GPU work overlaps (other streams, graphs replayed at the same time)
+ * need handles of their own.
+ */
+kld_status_t kld_beam_create(kld_beam_t* out, int max_groups, int max_beams, int max_k, int device);
+void kld_beam_destroy(kld_beam_t h);
+
+/*
+ * One step of beam search. logits: [groups * beams, V] device rows, `ld`
+ * elements apart (ld >= V), `dtype`, aligned to the element size. scores:
+ * [groups, beams] fp32 running log-probabilities; -inf: no such beam (its
+ * row is not read). finished (nullable): [groups, beams] bytes; a finished
+ * beam's row is not read and offers one candidate, token `eos` at its own
+ * score. Every other beam w offers each token j at
+ *   c = scores[w] + logits[w][j] - ln sum_i e^logits[w][i]
+ * (-inf logits offer nothing). Per group the k largest c, best first, ties to
+ * the lowest w * V + j, go to scores_out (c rounded to fp32), tokens_out and
+ * parents_out (the beam w), each [groups, k]; places without a candidate
+ * hold -inf, -1, -1. A row with NaN or +inf logits, or without an entry
+ * above -inf, offers nothing (KLD_BEAM_NONFINITE), nor does a beam whose
+ * score is NaN or +inf (KLD_BEAM_BAD_SCORE). The order is decided by c in
+ * fp64. The outputs may not overlap the inputs. beams * V < 2^32,
+ * 0 <= eos < V when finished is given. Asynchronous on `stream`; allocates
+ * nothing, so it may be captured into a graph.
+ */
+kld_status_t kld_beam_select(kld_beam_t h, const void* logits, int64_t ld, kld_dtype_t dtype,
+                             const float* scores, const uint8_t* finished, int32_t eos, int groups,
+                             int beams, int64_t V, int k, float* scores_out, int32_t* tokens_out,
+                             int32_t* parents_out, void* stream);
+
+/*
+ * One state of every beam, in device memory: row r (of groups * beams) at
+ * data + r * row_stride bytes holds `outer` runs, outer_stride bytes apart,
+ * each of `positions` positions of position_bytes contiguous bytes (a cache
+ * [rows, heads, time, dim]: outer = heads, positions = time; a state without
+ * a time axis: one position). timed: lengths apply to it.
+ */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t outer;
+  int64_t outer_stride;
+  int64_t positions;
+  int64_t position_bytes;
+  int32_t timed;
+  int32_t reserved;
+} kld_state_t;
+
+/*
+ * Reorder n states in place: beam w of group g takes over the state of beam
+ * parents[g][w] (as it was before the call). lengths (nullable, int32 per
+ * row): of a timed state's runs only the first lengths[row of the parent]
+ * positions are copied; what lies behind them stays as it was. A parent of -1
+ * leaves the beam as it is, any other parent outside [0, beams) does too and
+ * sets KLD_BEAM_BAD_PARENT. `states` is a HOST array, read during the call;
+ * the states, parents and lengths may not overlap one another.
+ * Asynchronous on `stream`; may be captured into a graph.
+ */
+kld_status_t kld_beam_reorder(kld_beam_t h, const kld_state_t* states, int n,
+                              const int32_t* parents, const int32_t* lengths, int groups,
+                              int beams, void* stream);
+
+#define KLD_BEAM_NONFINITE  (1u << 0)
+#define KLD_BEAM_BAD_SCORE  (1u << 1)
+#define KLD_BEAM_BAD_PARENT (1u << 2)
+
+/* Wait for this handle's last call and return (and clear) the KLD_BEAM_* bits
+ * its calls have met since the last time. */
+kld_status_t kld_beam_status(kld_beam_t h, uint32_t* flags);
 
 /* ======================================================================
  * Diagnostics. None of these computes anything the pages define: they

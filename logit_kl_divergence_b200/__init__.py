@@ -16,11 +16,15 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (KLD_BF16, KLD_F16, KLD_F32, ROW_BAD_TOKEN, ROW_EMPTY,  # noqa: F401
-                   ROW_INF_KL, ROW_INF_NLL, ROW_INF_NLL_BASE, ROW_NONFINITE, KLDError)
+from ._lib import (BEAM_BAD_PARENT, BEAM_BAD_SCORE, BEAM_NONFINITE, KLD_BF16,  # noqa: F401
+                   KLD_F16, KLD_F32, ROW_BAD_TOKEN, ROW_EMPTY, ROW_INF_KL, ROW_INF_NLL,
+                   ROW_INF_NLL_BASE, ROW_NONFINITE, KLDError)
+from .beam import BeamSearch, BeamStates
+from .packed import PACK_BLOCK, PackedLogits, _on, pack_logits
 
 __all__ = ["KLDStats", "kld_stats", "run_static", "result_from_bytes", "plan", "dtype_code",
-           "ROW_RECORD_BYTES", "selftest_bounded_wait"]
+           "ROW_RECORD_BYTES", "selftest_bounded_wait", "PackedLogits", "pack_logits", "PACK_BLOCK",
+           "BeamSearch", "BeamStates"]
 
 ROW_RECORD_BYTES = 40
 PARTIAL_BYTES = 64
@@ -137,6 +141,72 @@ class KLDStats:
                                           ctypes.c_void_p(_stream_ptr(stream, base.device)))
         _lib.check(st, "kld_stats_run_grad")
         return out
+
+    def _packed_call(self, base: PackedLogits, quant, token_ids, per_row, stream):
+        """Checks and marshals what run_packed and run_grad_packed share."""
+        if not isinstance(base, PackedLogits):
+            raise TypeError("base must be a PackedLogits")
+        n, vocab = base.shape
+        if base.device != self.device or quant.device != self.device:
+            raise ValueError("base and quant must be on the handle's device")
+        if tuple(quant.shape) != base.shape:
+            raise ValueError("base and quant must have the same shape")
+        dense, packed, dt = None, None, KLD_F32
+        if isinstance(quant, PackedLogits):
+            packed = ctypes.byref(quant._c)
+        else:
+            dt = dtype_code(quant)
+            if not quant.is_contiguous():
+                raise ValueError("quant must be contiguous")
+            dense = _ptr(quant)
+        if token_ids is not None:
+            if token_ids.dtype != torch.int32 or token_ids.dim() != 1 or token_ids.shape[0] != n:
+                raise ValueError("token_ids must be an int32 [N] tensor")
+            if not token_ids.is_contiguous() or token_ids.device != self.device:
+                raise ValueError("token_ids must be contiguous and on the handle's device")
+        s, ctx = _on(stream, self.device)
+        rows, fields = None, None
+        if per_row:
+            with ctx:
+                f64 = torch.empty((2, n), dtype=torch.float64, device=self.device)
+                i32 = torch.empty((2, n), dtype=torch.int32, device=self.device)
+            rows = {"kld": f64[0], "nll": f64[1], "amax_b": i32[0], "amax_q": i32[1]}
+            fields = ctypes.byref(_lib.Fields(*(t.data_ptr() for t in rows.values())))
+        head = (self._h, ctypes.byref(base._c), dense, dt, packed, _ptr(token_ids), n, vocab)
+        return head, fields, rows, s, ctx
+
+    def run_packed(self, base: PackedLogits, quant, token_ids: torch.Tensor | None = None,
+                   per_row: bool = False, stream=None) -> dict | None:
+        """:meth:`run` with the base rows read from an 8-bit checkpoint; the
+        quant rows are a dense [N, V] tensor (any of the three dtypes) or a
+        checkpoint too. The statistic is that of the stored values. With
+        ``per_row``, returns ``kld`` and ``nll`` (float64), ``amax_b`` and
+        ``amax_q`` (int32) as CUDA tensors of N values. Asynchronous on the
+        stream."""
+        head, fields, rows, s, _ = self._packed_call(base, quant, token_ids, per_row, stream)
+        _lib.check(self._lib.kld_stats_run_packed(*head, fields, ctypes.c_void_p(s.cuda_stream)),
+                   "kld_stats_run_packed")
+        return rows
+
+    def run_grad_packed(self, base: PackedLogits, quant, token_ids: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, scale: float = 1.0, grad_dtype=None,
+                        per_row: bool = False, stream=None):
+        """:meth:`run_packed` plus the gradient with respect to the quant
+        logits, as :meth:`run_grad` gives it (``grad_dtype``: the quant
+        logits' by default, float32 for packed ones), from one read of the
+        rows. Returns the gradient, or (gradient, rows) with ``per_row``.
+        Asynchronous on the stream."""
+        head, fields, rows, s, ctx = self._packed_call(base, quant, token_ids, per_row, stream)
+        if out is None:
+            dt = grad_dtype or (torch.float32 if isinstance(quant, PackedLogits) else quant.dtype)
+            with ctx:
+                out = torch.empty(base.shape, dtype=dt, device=self.device)
+        if tuple(out.shape) != base.shape or not out.is_contiguous() or out.device != self.device:
+            raise ValueError("out must be a contiguous [N, V] tensor on the logits' device")
+        _lib.check(self._lib.kld_stats_run_grad_packed(*head, _ptr(out), dtype_code(out), float(scale), fields,
+                                                       ctypes.c_void_p(s.cuda_stream)),
+                   "kld_stats_run_grad_packed")
+        return (out, rows) if per_row else out
 
     def run_topk(self, base: torch.Tensor, quant: torch.Tensor, token_ids: torch.Tensor | None = None,
                  k: int = 128, stream=None) -> dict:

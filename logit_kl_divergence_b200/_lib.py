@@ -28,6 +28,12 @@ KLD_STATIC_MAX_ROWS = 65536
 KLD_F32, KLD_BF16, KLD_F16 = 0, 1, 2
 KLD_PARTIAL_BYTES = 64
 KLD_MAX_TOPK = 1024
+KLD_PACK_BLOCK = 128
+KLD_BEAM_MAX_BEAMS = 64
+KLD_BEAM_MAX_K = 128
+BEAM_NONFINITE = 1 << 0
+BEAM_BAD_SCORE = 1 << 1
+BEAM_BAD_PARENT = 1 << 2
 
 ROW_NONFINITE = 1 << 0
 ROW_EMPTY = 1 << 1
@@ -93,11 +99,34 @@ class Plan(ctypes.Structure):
     ]
 
 
+class Packed(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("heads", ctypes.c_void_p)]
+
+
+class Fields(ctypes.Structure):
+    _fields_ = [("kld", ctypes.c_void_p), ("nll", ctypes.c_void_p), ("amax_b", ctypes.c_void_p),
+                ("amax_q", ctypes.c_void_p)]
+
+
+class State(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("outer", ctypes.c_int64),
+        ("outer_stride", ctypes.c_int64),
+        ("positions", ctypes.c_int64),
+        ("position_bytes", ctypes.c_int64),
+        ("timed", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 assert ctypes.sizeof(Row) == 40
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int
 _ST = ctypes.c_int
+_PK = ctypes.POINTER(Packed)
 
 # name -> (restype, argtypes); the same set the header declares.
 SIGNATURES = {
@@ -127,6 +156,17 @@ SIGNATURES = {
     "kld_stats_merge_partials": (_ST, [_P, _P, _I32, _I64, _P, _I64, _P]),
     "kld_stats_timing": (_ST, [_P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     "kld_plan": (_ST, [_I64, _I64, _I32, _I32, ctypes.POINTER(Plan)]),
+    "kld_pack_logits": (_ST, [_P, _I64, _I64, _I32, _PK, _I32, _P]),
+    "kld_unpack_logits": (_ST, [_PK, _I64, _I64, _P, _I32, _I32, _P]),
+    "kld_stats_run_packed": (_ST, [_P, _PK, _P, _I32, _PK, _P, _I64, _I64, ctypes.POINTER(Fields), _P]),
+    "kld_stats_run_grad_packed": (_ST, [_P, _PK, _P, _I32, _PK, _P, _I64, _I64, _P, _I32,
+                                        ctypes.c_double, ctypes.POINTER(Fields), _P]),
+    "kld_beam_create": (_ST, [ctypes.POINTER(_P), _I32, _I32, _I32, _I32]),
+    "kld_beam_destroy": (None, [_P]),
+    "kld_beam_select": (_ST, [_P, _P, _I64, _I32, _P, _P, ctypes.c_int32, _I32, _I32, _I64, _I32,
+                              _P, _P, _P, _P]),
+    "kld_beam_reorder": (_ST, [_P, ctypes.POINTER(State), _I32, _P, _P, _I32, _I32, _P]),
+    "kld_beam_status": (_ST, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "kld_stats_run_static": (_ST, [_P, _P, _P, _I64, _I64, _I32, _P, _P]),
 }
 

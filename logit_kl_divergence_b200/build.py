@@ -49,7 +49,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
+    cmd = [_nvcc(), *ARCH_FLAGS, "--threads", "0", "-O3", "-lineinfo", "-std=c++17",
            "-Xcompiler", "-fPIC,-O2", "-shared", "-cudart", "static",
            "-I", INCLUDE, "-I", CSRC, *sources(), "-o", tmp]
     if verbose:

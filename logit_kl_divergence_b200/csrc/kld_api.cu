@@ -13,12 +13,24 @@
 #include <cstring>
 #include <string>
 
+#include "kld_host.h"
 #include "kld_internal.h"
 #include "kld_probe.h"
 
 namespace {
 
 thread_local std::string g_last_cuda_error;
+
+using kld::cuda_fail;
+using kld::DeviceGuard;
+
+// Host-path staging: two buffers, each holding a chunk of base rows, quant
+// rows and token ids.
+constexpr size_t kStageTargetBytes = 128ull << 20;  // per operand per buffer
+
+}  // namespace
+
+namespace kld {
 
 kld_status_t cuda_fail(cudaError_t e, const char* what) {
   g_last_cuda_error = std::string(what) + ": " + cudaGetErrorString(e);
@@ -29,36 +41,26 @@ kld_status_t cuda_fail(cudaError_t e, const char* what) {
   return KLD_ERR_CUDA;
 }
 
-#define KLD_CUDA(call)                                 \
-  do {                                                 \
-    cudaError_t _e = (call);                           \
-    if (_e != cudaSuccess) return cuda_fail(_e, #call); \
-  } while (0)
-
-// Makes the handle's device current for the duration of a call.
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    ok_ = cudaGetDevice(&prev_) == cudaSuccess;
-    if (ok_ && prev_ != dev) ok_ = cudaSetDevice(dev) == cudaSuccess;
-    switched_ = ok_ && prev_ != dev;
+kld_status_t check_device(int device, int* sms) {
+  int ndev = 0;
+  cudaError_t e = cudaGetDeviceCount(&ndev);
+  if (e != cudaSuccess || ndev == 0) {
+    g_last_cuda_error = e != cudaSuccess ? cudaGetErrorString(e) : "no CUDA device";
+    return KLD_ERR_NO_DEVICE;
   }
-  ~DeviceGuard() {
-    if (switched_) cudaSetDevice(prev_);
+  if (device >= ndev) return KLD_ERR_INVALID_ARG;
+  int major = 0, minor = 0;
+  KLD_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device));
+  KLD_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device));
+  KLD_CUDA(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device));
+  if (major != 10 || minor != 0) {
+    g_last_cuda_error = "device is not compute capability 10.0";
+    return KLD_ERR_NO_DEVICE;
   }
-  bool ok() const { return ok_; }
+  return KLD_OK;
+}
 
- private:
-  int prev_ = 0;
-  bool ok_ = false;
-  bool switched_ = false;
-};
-
-// Host-path staging: two buffers, each holding a chunk of base rows, quant
-// rows and token ids.
-constexpr size_t kStageTargetBytes = 128ull << 20;  // per operand per buffer
-
-}  // namespace
+}  // namespace kld
 
 struct kld_stats_s {
   int device = 0;
@@ -161,6 +163,64 @@ kld_status_t run_statistic(kld_stats_t h, const void* base, const void* quant, c
   return KLD_OK;
 }
 
+// The statistic with packed base rows, and the gradient when grad is set.
+kld_status_t run_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
+                        kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,
+                        const int32_t* tok, int64_t N, int64_t V, void* grad,
+                        kld_dtype_t grad_dtype, float scale, const kld_fields_t* fields,
+                        void* stream) {
+  if (!h || !base || N < 1 || V < 1 || V > INT32_MAX || N > h->max_rows) return KLD_ERR_INVALID_ARG;
+  auto bad = [](const kld_packed_t* p) {
+    return !p->codes || !p->heads || (reinterpret_cast<uintptr_t>(p->codes) & 15u) ||
+           (reinterpret_cast<uintptr_t>(p->heads) & 3u);
+  };
+  if (bad(base) || (quant_packed && bad(quant_packed))) return KLD_ERR_INVALID_ARG;
+  if (!quant_packed) {
+    if (!valid_dtype(quant_dtype)) return KLD_ERR_DTYPE;
+    if (!quant || reinterpret_cast<uintptr_t>(quant) % kld::elem_bytes(quant_dtype))
+      return KLD_ERR_INVALID_ARG;
+  }
+  if (tok && (reinterpret_cast<uintptr_t>(tok) & 3u)) return KLD_ERR_INVALID_ARG;
+  const kld_fields_t none = {nullptr, nullptr, nullptr, nullptr};
+  const kld_fields_t& f = fields ? *fields : none;
+  if ((reinterpret_cast<uintptr_t>(f.kld) | reinterpret_cast<uintptr_t>(f.nll)) & 7u)
+    return KLD_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(f.amax_b) | reinterpret_cast<uintptr_t>(f.amax_q)) & 3u)
+    return KLD_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  h->timing_valid = h->timing;
+  h->rows_pending = false;
+  h->grad_timing_valid = false;
+  h->threshold_timed = false;
+  kld::PackedRows a;
+  a.base_codes = base->codes;
+  a.base_heads = base->heads;
+  a.quant = quant;
+  a.quant_dtype = quant_dtype;
+  a.quant_codes = quant_packed ? quant_packed->codes : nullptr;
+  a.quant_heads = quant_packed ? quant_packed->heads : nullptr;
+  a.token_ids = tok;
+  a.N = N;
+  a.V = V;
+  a.rows = h->rows;
+  a.kld = f.kld;
+  a.nll = f.nll;
+  a.amax_b = f.amax_b;
+  a.amax_q = f.amax_q;
+  a.grad = grad;
+  a.grad_dtype = grad_dtype;
+  a.scale = scale;
+  if (h->timing) KLD_CUDA(cudaEventRecord(h->tev[0], s));
+  KLD_CUDA(kld::launch_packed_rows(a, h->sm_count, s));
+  if (h->timing) KLD_CUDA(cudaEventRecord(h->tev[1], s));
+  h->last_rows = N;
+  h->last_stream = s;
+  h->rows_written = true;
+  return enqueue_reduce(h, h->rows, N, tok != nullptr, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -210,21 +270,9 @@ kld_status_t kld_stats_create(kld_stats_t* out, int64_t max_rows, int device) {
   if (!out) return KLD_ERR_INVALID_ARG;
   *out = nullptr;
   if (max_rows < 1 || device < 0) return KLD_ERR_INVALID_ARG;
-  int ndev = 0;
-  cudaError_t e = cudaGetDeviceCount(&ndev);
-  if (e != cudaSuccess || ndev == 0) {
-    g_last_cuda_error = e != cudaSuccess ? cudaGetErrorString(e) : "no CUDA device";
-    return KLD_ERR_NO_DEVICE;
-  }
-  if (device >= ndev) return KLD_ERR_INVALID_ARG;
-  int major = 0, minor = 0, sms = 0;
-  KLD_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device));
-  KLD_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device));
-  KLD_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
-  if (major != 10 || minor != 0) {
-    g_last_cuda_error = "device is not compute capability 10.0";
-    return KLD_ERR_NO_DEVICE;
-  }
+  int sms = 0;
+  const kld_status_t dev = kld::check_device(device, &sms);
+  if (dev != KLD_OK) return dev;
   DeviceGuard guard(device);
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   KLD_CUDA(kld::prepare_rows_kernels());
@@ -397,6 +445,29 @@ kld_status_t kld_stats_run_grad(kld_stats_t h, const void* base, const void* qua
                             static_cast<float>(scale), h->sm_count, s));
   if (h->timing) KLD_CUDA(cudaEventRecord(h->tev[3], s));
   return KLD_OK;
+}
+
+kld_status_t kld_stats_run_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
+                                  kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,
+                                  const int32_t* token_ids, int64_t N, int64_t V,
+                                  const kld_fields_t* fields, void* stream) {
+  return run_packed(h, base, quant, quant_dtype, quant_packed, token_ids, N, V, nullptr, KLD_F32,
+                    1.f, fields, stream);
+}
+
+kld_status_t kld_stats_run_grad_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
+                                       kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,
+                                       const int32_t* token_ids, int64_t N, int64_t V, void* grad,
+                                       kld_dtype_t grad_dtype, double scale,
+                                       const kld_fields_t* fields, void* stream) {
+  if (!h) return KLD_ERR_INVALID_ARG;
+  if (!valid_dtype(grad_dtype)) return KLD_ERR_DTYPE;
+  if (!grad || (reinterpret_cast<uintptr_t>(grad) % kld::elem_bytes(grad_dtype)))
+    return KLD_ERR_INVALID_ARG;
+  const float s = static_cast<float>(scale);
+  if (!(s - s == 0.f)) return KLD_ERR_INVALID_ARG;  // NaN or infinite, as fp32 too
+  return run_packed(h, base, quant, quant_dtype, quant_packed, token_ids, N, V, grad, grad_dtype, s,
+                    fields, stream);
 }
 
 kld_status_t kld_stats_run_partials(kld_stats_t h, const void* base, const void* quant,

@@ -210,6 +210,67 @@ cudaError_t launch_topk(const void* base, const void* quant, const RowAux* aux, 
 cudaError_t launch_topk_threshold(const void* base, int64_t N, int64_t V, kld_dtype_t dtype,
                                   int k, float* tf, int sm_count, cudaStream_t stream);
 
+// 8-bit logit checkpoints (format: kld_packed.cuh): codes [N, nb * 128]
+// (16-byte aligned), headers [N, nb], nb = ceil(V / 128).
+cudaError_t launch_pack(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+                        uint8_t* codes, uint32_t* heads, int sm_count, cudaStream_t stream);
+cudaError_t launch_unpack(const uint8_t* codes, const uint32_t* heads, int64_t N, int64_t V,
+                          void* out, kld_dtype_t out_dtype, int sm_count, cudaStream_t stream);
+
+// Row pass with packed base rows (and, when grad is set, the gradient in the
+// same kernel): dense quant rows, or a checkpoint of them when quant_codes is
+// set. Writes records and, where given, per-field copies.
+struct PackedRows {
+  const uint8_t* base_codes;
+  const uint32_t* base_heads;
+  const void* quant;
+  kld_dtype_t quant_dtype;
+  const uint8_t* quant_codes;
+  const uint32_t* quant_heads;
+  const int32_t* token_ids;
+  int64_t N, V;
+  kld_row_t* rows;
+  double* kld;
+  double* nll;
+  int32_t* amax_b;
+  int32_t* amax_q;
+  void* grad;
+  kld_dtype_t grad_dtype;
+  float scale;
+};
+cudaError_t launch_packed_rows(const PackedRows& a, int sm_count, cudaStream_t stream);
+
+// Beam selection (see kld_beam_select). Workspace: sums and counts of
+// `parts` entries, entries of parts * cap, parts <= 16 * SMs + 2 * rows;
+// tickets: one per group, zero between launches; flags: KLD_BEAM_* bits.
+struct BeamPlan {
+  int parts;      // CTAs per row
+  int64_t slice;  // columns of each
+};
+BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count);
+struct BeamSelect {
+  const void* logits;
+  int64_t ld;
+  kld_dtype_t dtype;
+  const float* scores;
+  const uint8_t* finished;
+  int32_t eos;
+  int groups, beams, k, cap;
+  int64_t V;
+  float2* sums;
+  int* counts;
+  float2* entries;
+  unsigned* tickets;
+  uint32_t* flags;
+  float* out_scores;
+  int32_t* out_tokens;
+  int32_t* out_parents;
+};
+cudaError_t launch_beam_select(const BeamSelect& b, int sm_count, cudaStream_t stream);
+cudaError_t launch_beam_reorder(const kld_state_t* states, int n, const int32_t* parents,
+                                const int32_t* lengths, int groups, int beams, uint32_t* flags,
+                                cudaStream_t stream);
+
 // Bounded-wait self-test (see kld_selftest_bounded_wait).
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int use_abort, uint32_t* derr,
                                  unsigned long long* waited_ns, cudaStream_t stream);

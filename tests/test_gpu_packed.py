@@ -1,0 +1,331 @@
+"""8-bit logit checkpoints on the GPU.
+
+Codes, headers and restored fp32 values: equal bit for bit to the format's
+definition in 64 bits (its arithmetic is exact in fp32, so no tolerance).
+16-bit restored values: the fp32 ones rounded to nearest.
+
+Statistic from a checkpoint: that of the stored values by the fp64 oracle, at
+the bars of gpu_helpers (per-row KL and NLL |d| <= 1e-6 + 1e-4 |ref|, argmaxes,
+flags and counts equal).
+
+Gradient: every element within |scale| * (4e-6 * (p + r) + 1e-12), p and r its
+two softmax values. Each is an fp32 exponential: its argument u = x L - F is
+one FMA (error <= |u| 2^-24, that is <= |u| ln2 2^-24 = 1.7e-6 relative at
+|u| = 40, where the value is 1e-12), ex2.approx 2^-22, lambda - 1 = 1.4e-8
+times |u|, the normaliser's sum (a few hundred fp32 terms whose partial sums
+round by 2^-24 each, ~1e-6 in the worst case, and fp64 from there) and its
+rounding 2^-24: <= 3.5e-6 together. Outputs in 16 bits add half a step, 2^-8
+(bf16) or 2^-11 (fp16) of the value, and fp16's fixed step 2^-25 below its
+normal range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import packed_ref
+from logit_kl_divergence_b200 import KLDStats, PackedLogits, pack_logits, rows_view, synth
+
+from gpu_helpers import assert_rows_match, assert_stats_match
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy()
+
+
+def _pair(n, v, seed, masked=0):
+    g = torch.Generator().manual_seed(seed)
+    b = torch.randn((n, v), generator=g) * 2.5
+    b[torch.arange(n), torch.randint(0, v, (n,), generator=g)] += 9.0
+    q = b + torch.randn((n, v), generator=g) * 0.2
+    if masked:
+        b[:, v - masked:] = -math.inf
+        q[:, v - masked:] = -math.inf
+    tok = torch.randint(0, max(1, v - masked), (n,), generator=g, dtype=torch.int32)
+    return b, q, tok
+
+
+def _check_pack(x):
+    p = pack_logits(x.to(DEV))
+    codes, heads, value = packed_ref.pack(_np(x))
+    assert np.array_equal(p.heads.cpu().numpy(), heads)
+    assert np.array_equal(p.codes.cpu().numpy(), codes)
+    back = p.unpack()
+    assert np.array_equal(_np(back), value.astype(np.float32), equal_nan=True)
+    for dt in (torch.bfloat16, torch.float16):
+        got = p.unpack(dt)
+        want = back.to(dt)
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+    return p
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,v", [(1, 1), (3, 7), (2, 127), (5, 128), (4, 129), (7, 1000), (3, 4099),
+                                 (2, 32003), (33, 512), (1, 70001)])
+def test_pack_and_unpack_are_the_format(dtype, n, v):
+    _check_pack(_pair(n, v, 3 * v + n)[0].to(DTYPES[dtype]))
+
+
+def test_pack_of_masks_and_odd_values():
+    b, _, _ = _pair(12, 1000, 5, masked=300)
+    b[1] = -math.inf                       # a fully masked row
+    b[2] = 1000.125                        # a constant: stored exactly
+    b[3] = 0.0
+    b[4] = torch.finfo(torch.float32).min  # magnitudes past the format's limit
+    b[5, 17] = math.nan
+    b[6, 130] = math.inf
+    b[7] = torch.randn(1000) * 1e-42       # subnormals
+    b[8] = torch.randn(1000) * 1e30
+    b[9] = torch.where(torch.arange(1000) % 3 == 0, torch.tensor(-math.inf), b[9])
+    b[10] = torch.arange(1000).float() * 254.0 / 127.0  # ends on whole steps
+    b[11] = 2.0 ** 126 * torch.where(torch.arange(1000) == 5, 1.0, 0.999)
+    p = _check_pack(b)
+    assert torch.equal(p.unpack()[2].cpu(), b[2])
+
+
+def test_pack_writes_parts_of_a_store_and_nothing_else():
+    b, _, _ = _pair(6, 333, 8)
+    store = PackedLogits.empty(10, 333, DEV)
+    store.codes.fill_(77)
+    store.heads.fill_(99)
+    pack_logits(b.to(DEV), out=store.rows(2, 8))
+    whole = pack_logits(b.to(DEV))
+    assert torch.equal(store.codes[2:8], whole.codes) and torch.equal(store.heads[2:8], whole.heads)
+    for part in (slice(0, 2), slice(8, 10)):
+        assert (store.codes[part] == 77).all() and (store.heads[part] == 99).all()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_pack_of_a_row_that_starts_inside_a_vector(dtype):
+    dt = DTYPES[dtype]
+    b, _, _ = _pair(5, 1001, 9)
+    for shift in range(1, 8):
+        flat = torch.empty(5 * 1001 + 8, dtype=dt, device=DEV)
+        x = flat[shift:shift + 5 * 1001].view(5, 1001)
+        x.copy_(b)
+        want = pack_logits(b.to(dt).to(DEV).clone())
+        got = pack_logits(x)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.heads, want.heads)
+
+
+# ---------------------------------------------------------- statistic, gradient
+
+def _tolerance(p, r, ref, dtype, scale):
+    tol = abs(scale) * (4e-6 * (np.nan_to_num(p) + np.nan_to_num(r)) + 1e-12)
+    if dtype == torch.bfloat16:
+        tol = tol + np.abs(ref) * 2.0 ** -8
+    elif dtype == torch.float16:
+        tol = tol + np.maximum(np.abs(ref) * 2.0 ** -11, 2.0 ** -25)
+    return tol
+
+
+def _check(b, q, tok, quant="f32", grad=None, scale=1.0, out=None, pack_quant=False):
+    n, v = b.shape
+    base = pack_logits(b.to(DEV))
+    qd = q.to(DTYPES[quant]).to(DEV)
+    other = pack_logits(qd) if pack_quant else qd
+    t = None if tok is None else tok.to(DEV)
+    with KLDStats(n, DEV) as st:
+        if grad is None:
+            rows = st.run_packed(base, other, t, per_row=True)
+            g = None
+        else:
+            g, rows = st.run_grad_packed(base, other, t, out=out, scale=scale, grad_dtype=DTYPES[grad],
+                                         per_row=True)
+        res = st.result()
+        rec = {k: x.cpu().numpy() for k, x in rows_view(st.records()).items()}
+    rec["flags"] = rec["flags"].astype(np.uint32)
+    bv, qv = base.unpack().cpu(), (other.unpack() if pack_quant else qd.float()).cpu()
+    ref_rows, ref = oracle.run(bv, qv, tok, oracle.F32)
+    # rows of the type's lowest value: the oracle's q - lse_q absorbs ln V there
+    # (it gives a negative KL), so they are taken relative to the maximum
+    for i in np.nonzero((qv.amax(1) < -1e37).numpy() & ((ref_rows["flags"] & 3) == 0))[0]:
+        ref_rows["kld"][i], lp, lr = packed_ref.relative_row(bv[i].numpy(), qv[i].numpy())
+        if tok is not None and 0 <= tok[i] < v:
+            ref_rows["nll"][i], ref_rows["nll_base"][i] = -lr[tok[i]], -lp[tok[i]]
+        ref = oracle.reduce(ref_rows, tok is not None)
+    assert_rows_match(rec, ref_rows)
+    assert_stats_match(res, ref)
+    for name in ("kld", "nll", "amax_b", "amax_q"):
+        assert np.array_equal(rows[name].cpu().numpy(), rec[name], equal_nan=True)
+    if g is not None:
+        p, r = packed_ref.softmax(bv.numpy()), packed_ref.softmax(qv.numpy())
+        keep = (ref_rows["flags"] & 3) == 0
+        want = np.where(keep[:, None], (r - p) * scale, 0.0)
+        got = _np(g).astype(np.float64)
+        d = np.abs(got - want)
+        tol = _tolerance(p, r, want, g.dtype, scale)
+        assert (d <= tol).all(), (d / tol).max()
+        assert (got[~keep] == 0).all()
+    return rec
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "f16", "packed"])
+@pytest.mark.parametrize("n,v", [(1, 1), (3, 2), (5, 7), (4, 129), (9, 512), (3, 513), (2, 1000),
+                                 (5, 4099), (2, 32003), (1, 151936), (3, 70001)])
+def test_statistic_and_gradient(n, v, quant):
+    b, q, tok = _pair(n, v, v + n)
+    dt = "f32" if quant == "packed" else quant
+    _check(b, q, tok, dt, None, pack_quant=quant == "packed")
+    _check(b, q, tok, dt, dt, scale=1.0 / n, pack_quant=quant == "packed")
+
+
+@pytest.mark.parametrize("quant,grad", [("f32", "bf16"), ("f32", "f16"), ("bf16", "f32"),
+                                        ("f16", "f32"), ("bf16", "f16"), ("packed", "f32"),
+                                        ("packed", "bf16"), ("packed", "f16")])
+@pytest.mark.parametrize("v", [1024, 2051])
+def test_gradient_of_another_type(quant, grad, v):
+    b, q, tok = _pair(6, v, v, masked=40)
+    _check(b, q, tok, "f32" if quant == "packed" else quant, grad, scale=0.25, pack_quant=quant == "packed")
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+def test_many_rows_take_whole_and_split_launches(quant):
+    for n, v in ((40, 20000), (300, 9001), (700, 1536)):
+        b, q, tok = _pair(n, v, n)
+        _check(b, q, tok, "f32" if quant == "packed" else quant, "f32", scale=1.0, pack_quant=quant == "packed")
+
+
+def _edge_rows(v):
+    b, q, tok = _pair(16, v, 77)
+    b[0, v // 2:] = -math.inf
+    q[0, v // 2:] = -math.inf                    # masks in both
+    b[1, :v // 3] = -math.inf                    # masked in the base only
+    q[2, 3] = -math.inf                          # KL = +inf
+    b[3] = -math.inf                             # empty rows
+    q[4] = -math.inf
+    q[5, v - 1] = math.nan
+    q[6, 0] = math.inf
+    b[7, v // 2] = math.nan
+    q[8] = b[8] + 1000.0                         # a constant shift
+    q[9] = torch.finfo(torch.float32).min        # the type's lowest value everywhere
+    q[10, ::2] = torch.finfo(torch.float32).min  # and as a mask
+    b[10, ::2] = -math.inf
+    b[11] = 0.0
+    q[11] = 0.0                                  # ties everywhere
+    b[12, 5] += 80.0
+    q[12, 5] += 80.0                             # one-hot
+    q[13] = b[13]
+    tok[14], tok[15] = -1, v
+    tok[0] = v - 1                               # a masked token
+    tok[2] = 3
+    return b, q, tok
+
+
+@pytest.mark.parametrize("v", [40, 1500, 33000])
+@pytest.mark.parametrize("grad", [None, "f32"])
+def test_rows_at_the_edges(v, grad):
+    b, q, tok = _edge_rows(v)
+    _check(b, q, tok, "f32", grad)
+    _check(b, q, None, "f32", grad)
+
+
+@pytest.mark.parametrize("v", [40, 1500])
+def test_rows_at_the_edges_with_both_packed(v):
+    b, q, tok = _edge_rows(v)
+    _check(b, q, tok, "f32", "f32", pack_quant=True)
+
+
+def test_equal_rows_give_zero_exactly():
+    b, _, tok = _pair(9, 5000, 4)
+    base = pack_logits(b.to(DEV))
+    with KLDStats(9, DEV) as st:
+        g, rows = st.run_grad_packed(base, base.unpack(), tok.to(DEV), per_row=True)
+        assert (g == 0).all() and (rows["kld"] == 0).all()
+        g, rows = st.run_grad_packed(base, base, tok.to(DEV), per_row=True)
+        assert (g == 0).all() and (rows["kld"] == 0).all()
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "f16"])
+def test_quant_rows_and_gradient_at_any_alignment(quant):
+    dt = DTYPES[quant]
+    n, v = 3, 1037
+    b, q, tok = _pair(n, v, 12, masked=9)
+    for shift in range(0, 8):
+        flat = torch.empty(n * v + 16, dtype=dt, device=DEV)
+        x = flat[shift:shift + n * v].view(n, v)
+        x.copy_(q)
+        store = torch.full((n * v + 32,), 7.0, dtype=torch.float32, device=DEV)
+        out = store[8 + shift:8 + shift + n * v].view(n, v)
+        base = pack_logits(b.to(DEV))
+        with KLDStats(n, DEV) as st:
+            got = st.run_grad_packed(base, x, tok.to(DEV), out=out)
+            want = st.run_grad_packed(base, q.to(dt).to(DEV), tok.to(DEV), grad_dtype=torch.float32)
+            # another order of the sums only: S differs by a few 2^-24
+            p = np.abs(packed_ref.softmax(_np(base.unpack()))) + np.abs(packed_ref.softmax(_np(x)))
+            assert (np.abs(_np(got) - _np(want)) <= 4e-6 * p + 1e-12).all()
+        assert (store[:8 + shift] == 7).all() and (store[8 + shift + n * v:] == 7).all()
+
+
+def test_gradient_agrees_with_differences():
+    # d KL / d q by central differences of the oracle in fp64 over the stored values
+    b, q, _ = _pair(1, 60, 3)
+    base = pack_logits(b.to(DEV))
+    with KLDStats(1, DEV) as st:
+        g = st.run_grad_packed(base, q.to(DEV))[0].cpu().double()
+    p = packed_ref.softmax(_np(base.unpack()))[0]
+    x = q[0].double().numpy()
+
+    def kl(z):
+        r = packed_ref.softmax(z[None])[0]
+        return float((p * (np.log(p) - np.log(r))).sum())
+
+    h = 1e-5
+    for j in range(60):
+        e = np.zeros(60)
+        e[j] = h
+        d = (kl(x + e) - kl(x - e)) / (2 * h)
+        # differences: h^2/6 of the third derivative (<= 1) + 1e-15 / h; gradient: as above
+        assert abs(float(g[j]) - d) <= 4e-6 * 2 + 1e-9
+
+
+def test_store_kept_across_steps_streams_and_graphs():
+    b, q, tok = _pair(24, 3000, 21)
+    base, t = pack_logits(b.to(DEV)), tok.to(DEV)
+    quant = q.to(DEV)
+    with KLDStats(24, DEV) as st:
+        want, rows = st.run_grad_packed(base, quant, t, scale=0.5, per_row=True)
+        want, kld = want.clone(), rows["kld"].clone()
+        res = st.result()
+        side = torch.cuda.Stream(DEV)
+        side.wait_stream(torch.cuda.current_stream(DEV))
+        got, rows = st.run_grad_packed(base, quant, t, scale=0.5, per_row=True, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(rows["kld"], kld) and st.result() == res
+        # captured and replayed on new quant rows
+        out = torch.empty_like(want)
+        moving = quant.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            st.run_grad_packed(base, moving, t, out=out, scale=0.5)
+        moving.copy_(quant.flip(1))
+        want2 = st.run_grad_packed(base, quant.flip(1).contiguous(), t, scale=0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want2)
+        moving.copy_(quant)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_packed_rows_leave_the_dense_path_as_it_was():
+    w = synth.make_recipe("ctx", n=40, v=2049, dtype=synth.F32, seed=3)
+    b, q, t = w.base.to(DEV), w.quant.to(DEV), w.token_ids.to(DEV)
+    with KLDStats(40, DEV) as st:
+        st.run(b, q, t)
+        before = st.result()
+        st.run_grad_packed(pack_logits(b), q, t)
+        st.run(b, q, t)
+        assert st.result() == before
+
+
+def test_sizes_of_zero_rows():
+    p = pack_logits(torch.empty((0, 300), device=DEV))
+    assert p.shape == (0, 300) and p.unpack().shape == (0, 300)

@@ -1,0 +1,116 @@
+"""Arguments of the logit checkpoints and of beam search are refused before
+any GPU work. Runs without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from logit_kl_divergence_b200 import _lib, PackedLogits, pack_logits
+from logit_kl_divergence_b200.beam import BeamStates, _describe
+
+INVALID, DTYPE = _lib.KLD_ERR_INVALID_ARG, _lib.KLD_ERR_DTYPE
+P = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def _pk(codes=P, heads=P):
+    return ctypes.byref(_lib.Packed(codes, heads))
+
+
+def test_pack_and_unpack_refuse(lib):
+    x = ctypes.c_void_p(P)
+    for f in (lambda n=4, v=8, dt=0, x=x, pk=_pk(), dev=0: lib.kld_pack_logits(x, n, v, dt, pk, dev, None),
+              lambda n=4, v=8, dt=0, x=x, pk=_pk(), dev=0: lib.kld_unpack_logits(pk, n, v, x, dt, dev, None)):
+        assert f(n=0) == INVALID and f(v=0) == INVALID and f(v=1 << 31) == INVALID
+        assert f(n=1 << 60) == INVALID and f(dt=3) == DTYPE and f(dev=-1) == INVALID
+        assert f(x=None) == INVALID and f(x=ctypes.c_void_p(P + 2)) == INVALID
+        assert f(pk=None) == INVALID and f(pk=_pk(codes=None)) == INVALID
+        assert f(pk=_pk(heads=None)) == INVALID and f(pk=_pk(codes=P + 8)) == INVALID
+        assert f(pk=_pk(heads=P + 2)) == INVALID
+
+
+def test_packed_runs_and_beams_refuse_a_null_handle(lib):
+    x = ctypes.c_void_p(P)
+    assert lib.kld_stats_run_packed(None, _pk(), x, 0, None, None, 1, 1, None, None) == INVALID
+    assert lib.kld_stats_run_grad_packed(None, _pk(), x, 0, None, None, 1, 1, x, 0, 1.0, None, None) == INVALID
+    assert lib.kld_beam_select(None, x, 1, 0, x, None, 0, 1, 1, 1, 1, x, x, x, None) == INVALID
+    assert lib.kld_beam_reorder(None, None, 0, x, None, 1, 1, None) == INVALID
+    assert lib.kld_beam_status(None, ctypes.byref(ctypes.c_uint32())) == INVALID
+    lib.kld_beam_destroy(None)
+
+
+def test_beam_create_refuses_sizes(lib):
+    h = ctypes.c_void_p()
+    assert lib.kld_beam_create(None, 1, 1, 1, 0) == INVALID
+    for groups, beams, k, dev in ((0, 1, 1, 0), (1, 0, 1, 0), (1, 65, 1, 0), (1, 1, 0, 0), (1, 1, 129, 0),
+                                  (1, 1, 1, -1), (1 << 24, 2, 1, 0)):
+        assert lib.kld_beam_create(ctypes.byref(h), groups, beams, k, dev) == INVALID
+    if not torch.cuda.is_available():
+        assert lib.kld_beam_create(ctypes.byref(h), 1, 1, 1, 0) == _lib.KLD_ERR_NO_DEVICE
+
+
+def test_packed_logits_checks_its_tensors():
+    c, h = torch.zeros((3, 256), dtype=torch.uint8), torch.zeros((3, 2), dtype=torch.int32)
+    p = PackedLogits(c, h, 200)
+    assert p.shape == (3, 200) and len(p) == 3 and p.nbytes == 3 * 256 + 24
+    assert p.rows(1, 3).shape == (2, 200) and p.rows(2, 2).shape == (0, 200)
+    assert p.rows(1, 3).codes.data_ptr() == c[1].data_ptr()
+    for bad in ((c, h, 128), (c, h, 257), (c, h, 0), (c[:2], h, 200), (c.t(), h, 200)):
+        with pytest.raises(ValueError):
+            PackedLogits(*bad)
+    with pytest.raises(TypeError):
+        PackedLogits(c.int(), h, 200)
+    with pytest.raises(TypeError):
+        PackedLogits(c, h.long(), 200)
+    with pytest.raises(ValueError):
+        p.rows(2, 4)
+    with pytest.raises(ValueError):
+        p.unpack()  # not on a GPU
+    with pytest.raises(ValueError):
+        pack_logits(torch.zeros((2, 3)))
+    with pytest.raises(TypeError):
+        pack_logits(torch.zeros((2, 3), dtype=torch.float64))
+
+
+class _Cuda:
+    """A tensor's layout without its memory, for the host's description."""
+
+    def __init__(self, t):
+        self._t = t
+        self.is_cuda = True
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def _runs(t, time_dim):
+    s = _describe(_Cuda(t), time_dim)
+    return s.row_stride, s.outer, s.outer_stride, s.positions, s.position_bytes, s.timed
+
+
+def test_states_are_described_as_runs():
+    x = torch.zeros((6, 3, 10, 4))
+    assert _runs(x, 2) == (480, 3, 160, 10, 16, 1)
+    assert _runs(x, None) == (480, 1, 0, 1, 480, 0)
+    assert _runs(x, 1) == (480, 1, 0, 3, 160, 1)
+    y = torch.zeros((6, 10, 3, 4))
+    assert _runs(y.transpose(1, 2), 2) == (480, 1, 0, 10, 48, 1)  # heads seen before time
+    assert _runs(x[:, :, :7], 2) == (480, 3, 160, 7, 16, 1)       # part of a longer cache
+    assert _runs(x[:, 1], 1) == (480, 1, 0, 10, 16, 1)
+    assert _runs(torch.zeros((5,), dtype=torch.bfloat16), None) == (2, 1, 0, 1, 2, 0)
+    assert _runs(torch.zeros((4, 0)), None)[3:5] == (0, 0)
+    for bad, d in ((x[..., ::2], 2), (x[:, :, ::2], 2), (x.transpose(2, 3), 2), (x.transpose(1, 2), 1), (x, 0), (x, 4),
+                   (x[:, :, :, :3], None)):
+        with pytest.raises(ValueError):
+            _describe(_Cuda(bad), d)
+
+
+def test_bound_states_are_checked():
+    with pytest.raises(ValueError):
+        BeamStates([torch.zeros((2, 3))], torch.device("cpu"))  # not CUDA tensors
+    with pytest.raises(ValueError):
+        BeamStates([torch.zeros((2, 3)), torch.zeros((3, 3))], torch.device("cpu"))
