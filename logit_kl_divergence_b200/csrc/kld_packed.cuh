@@ -53,6 +53,14 @@ __device__ __forceinline__ Scale scale_of(uint32_t head) {
   s.masked = (head & 256u) != 0u && eb != 255u;
   return s;
 }
+// The same for a block without masks or bad values (bit 8 of its header is
+// 0), in a few integer and FMA-pipe operations: the step's bits are the low
+// byte less one in the exponent field; 1.5 * 2^23 + base is made by its bits.
+__device__ __forceinline__ void plain_scale(uint32_t head, float& step, float& off) {
+  step = __uint_as_float(head * 0x00800000u - 0x00800000u);
+  const float b = __uint_as_float(0x4b400000u + static_cast<uint32_t>(static_cast<int32_t>(head) >> 9));
+  off = (b - 20971520.f) * step;  // base - 2^23, exactly
+}
 // Byte k of w as the float 2^23 + byte.
 template <int K>
 __device__ __forceinline__ float magic_byte(uint32_t w) {

@@ -51,7 +51,8 @@ namespace from_packed {
 using namespace packed;
 
 constexpr int kFromPack = 3;  // quant operand from a checkpoint
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kCtasPerSm = 5;  // 20 warps of at most 96 registers
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 512;   // columns a warp takes at a time
 constexpr int kDepth = 4;     // chunks in flight per warp
@@ -62,12 +63,23 @@ constexpr uint32_t kExcludedFlags = KLD_ROW_NONFINITE | KLD_ROW_EMPTY;
 // ------------------------------------------------------------- small pieces
 
 // 2^d for a whole d <= 0 (0 below the normal range), exactly.
-__device__ __forceinline__ double pow2i(float d) {
+__device__ __forceinline__ double pow2d(float d) {
   return d < -1022.f ? 0.0
                      : __longlong_as_double(static_cast<long long>(static_cast<int>(d) + 1023) << 52);
 }
-__device__ __forceinline__ float max8(const float* x) {
-  return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+// The type whose quant values stay packed in the sums (see Packed), or 0.
+template <int QT>
+constexpr int kPacked16 = QT == KLD_BF16 || QT == KLD_F16 ? QT : 0;
+
+// Two values that are of the 16-bit type, packed.
+template <int QT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (QT == KLD_BF16) {
+    return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 __device__ __forceinline__ float sum_lanes(float x) {
 #pragma unroll
@@ -128,16 +140,16 @@ struct Outputs {
 };
 
 // Quant operand traits: bytes of one element, elements of a lane's
-// contiguous group and groups of a lane's 8-column step.
+// contiguous group and groups of a lane's 16 columns of a chunk.
 template <int QT>
 struct Quant {
   static constexpr int kBytes = QT == KLD_F32 ? 4 : (QT == kFromPack ? 1 : 2);
   static constexpr int kGroup = QT == KLD_F32 ? 4 : 8;
-  static constexpr int kGroups = 8 / kGroup;
+  static constexpr int kGroups = 16 / kGroup;
 };
-// A chunk's slot in shared memory: the codes (with the 16 bytes before them
-// when shifted), five headers from the chunk's first block - 1 on, and the
-// quant operand likewise.
+// A chunk's slot in shared memory: the codes and their blocks' headers (from
+// 16 codes and one block before the chunk on when shifted), and the quant
+// operand likewise.
 constexpr int kCodeBytes = kChunk + 16;
 constexpr int kHeadBytes = 32;
 template <int QT>
@@ -156,46 +168,88 @@ struct RowPtr {
   int off;                  // columns before the row in its first 16-byte vector
 };
 
-// Starts the copies of chunk c into a slot (one commit group, by all lanes).
+// What a lane copies of chunk 0; chunk c lies c * (bytes of a chunk) further.
+struct LanePtr {
+  const uint8_t* bcodes;
+  const uint32_t* bheads;
+  const char* quant;       // dense values, or codes
+  const uint32_t* qheads;
+};
 template <int QT, bool kOff>
-__device__ __forceinline__ void fetch(const RowPtr& rp, int64_t V, int64_t nb, int64_t c,
-                                      uint32_t slot, int lane) {
-  const int64_t col0 = c * kChunk;  // on the row's code grid; columns start at col0 - off
-  const int64_t coded = nb * kBlock;
-  {
-    const int64_t at = col0 + (lane - (kOff ? 1 : 0)) * 16;
-    if ((!kOff || at >= 0) && at < coded) copy16(slot + lane * 16, rp.bcodes + at);
-    if (kOff && lane == 0 && at + 512 < coded) copy16(slot + 512, rp.bcodes + at + 512);
-    if (lane < 5) {
-      const int64_t h = c * (kChunk / kBlock) + lane - 1;
-      if (h >= 0 && h < nb) {
-        copy4(slot + Slot<QT>::kHeads + lane * 4, rp.bheads + h);
-        if (QT == kFromPack) copy4(slot + Slot<QT>::kQuant + kCodeBytes + lane * 4, rp.qheads + h);
-      }
+__device__ __forceinline__ LanePtr lane_ptr(const RowPtr& rp, int lane) {
+  LanePtr p;
+  const int64_t at = static_cast<int64_t>(lane - (kOff ? 1 : 0)) * 16;
+  p.bcodes = rp.bcodes + at;
+  p.bheads = rp.bheads + lane - (kOff ? 1 : 0);
+  p.qheads = nullptr;
+  if (QT == kFromPack) {
+    p.quant = rp.quant + at;
+    p.qheads = rp.qheads + lane - (kOff ? 1 : 0);
+  } else {
+    p.quant = rp.quant + (lane * 16 - (kOff ? rp.off * Quant<QT>::kBytes : 0));
+  }
+  return p;
+}
+
+// Starts the copies of chunk c into a slot (all lanes; one commit group is
+// the caller's). inner: everything the chunk's copies read lies inside the
+// row's buffers; otherwise each copy is checked.
+template <int QT, bool kOff>
+__device__ __forceinline__ void fetch(const LanePtr& p, const RowPtr& rp, int64_t V, int64_t nb,
+                                      int c, bool inner, uint32_t slot, int lane) {
+  constexpr int kHeadsRead = kOff ? 5 : 4;
+  constexpr int kVecs = kChunk * Quant<QT>::kBytes / 512;  // 16-byte vectors a lane copies of dense rows
+  const uint8_t* bc = p.bcodes + static_cast<int64_t>(c) * kChunk;
+  const uint32_t* bh = p.bheads + static_cast<int64_t>(c) * (kChunk / kBlock);
+  const char* qc = p.quant + static_cast<int64_t>(c) * (kChunk * Quant<QT>::kBytes);
+  const uint32_t* qh = QT == kFromPack ? p.qheads + static_cast<int64_t>(c) * (kChunk / kBlock) : nullptr;
+  const uint32_t q = slot + Slot<QT>::kQuant;
+  if (inner) {
+    copy16(slot + lane * 16, bc);
+    if (kOff && lane == 0) copy16(slot + 512, bc + 512);
+    if (lane < kHeadsRead) {
+      copy4(slot + Slot<QT>::kHeads + lane * 4, bh);
+      if (QT == kFromPack) copy4(q + kCodeBytes + lane * 4, qh);
     }
     if (QT == kFromPack) {
-      const uint32_t q = slot + Slot<QT>::kQuant;
-      if ((!kOff || at >= 0) && at < coded) copy16(q + lane * 16, rp.quant + at);
-      if (kOff && lane == 0 && at + 512 < coded) copy16(q + 512, rp.quant + at + 512);
-    }
-  }
-  if (QT != kFromPack) {
-    constexpr int E = 16 / Quant<QT>::kBytes;
-    const int off = kOff ? rp.off : 0;
+      copy16(q + lane * 16, qc);
+      if (kOff && lane == 0) copy16(q + 512, qc + 512);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kChunk / E / 32; ++k) {
-      const int64_t j = col0 + (k * 32 + lane) * E - off;
-      if ((!kOff || j >= 0) && j + E <= V)
-        copy16(slot + Slot<QT>::kQuant + (k * 32 + lane) * 16, rp.quant + j * Quant<QT>::kBytes);
+      for (int k = 0; k < kVecs; ++k) copy16(q + k * 512 + lane * 16, qc + k * 512);
+    }
+    return;
+  }
+  const int64_t coded = nb * kBlock;
+  const int64_t at = static_cast<int64_t>(c) * kChunk + (lane - (kOff ? 1 : 0)) * 16;
+  const bool here = at >= 0 && at < coded, tail = kOff && lane == 0 && at + 512 < coded;
+  if (here) copy16(slot + lane * 16, bc);
+  if (tail) copy16(slot + 512, bc + 512);
+  const int64_t h = static_cast<int64_t>(c) * (kChunk / kBlock) + lane - (kOff ? 1 : 0);
+  if (lane < kHeadsRead && h >= 0 && h < nb) {
+    copy4(slot + Slot<QT>::kHeads + lane * 4, bh);
+    if (QT == kFromPack) copy4(q + kCodeBytes + lane * 4, qh);
+  }
+  if (QT == kFromPack) {
+    if (here) copy16(q + lane * 16, qc);
+    if (tail) copy16(q + 512, qc + 512);
+  } else {
+    constexpr int E = 16 / Quant<QT>::kBytes;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t j = static_cast<int64_t>(c) * kChunk + (k * 32 + lane) * E - (kOff ? rp.off : 0);
+      if (j >= 0 && j + E <= V) copy16(q + k * 512 + lane * 16, qc + k * 512);
     }
   }
 }
 
 // G (4 or 8) values of a checkpoint row from its slot: `at` is the first
-// column's offset in the chunk's code grid (at least -off for kOff).
-template <int G, bool kOff>
+// column's offset in the chunk's code grid (at least -off for kOff). Blocks
+// with masks or bad values (bit 8 of the headers, gathered in `special`) give
+// wrong values unless kMasks.
+template <int G, bool kOff, bool kMasks>
 __device__ __forceinline__ void slot_values(const unsigned char* codes, const uint32_t* heads,
-                                            int at, bool& masked, float* o) {
+                                            int at, uint32_t& special, float* o) {
   uint32_t w[G / 4 + 1];
   if (!kOff) {
     if (G == 8) {
@@ -213,21 +267,38 @@ __device__ __forceinline__ void slot_values(const unsigned char* codes, const ui
 #pragma unroll
     for (int k = 0; k < G / 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], bits);
   }
-  const Scale s = scale_of(heads[(at >> 7) + 1]);
-  masked |= s.masked;
+  const uint32_t* h = heads + (at >> 7) + (kOff ? 1 : 0);
+  const uint32_t h0 = h[0];
+  const int cut = kOff ? kBlock - (at & (kBlock - 1)) : G;  // columns of the first block
+  const uint32_t h1 = kOff && cut < G ? h[1] : h0;          // a group may cross into the next one
+  special |= h0 | h1;
+  if (kMasks) {
+    const Scale s = scale_of(h0), t = scale_of(h1);
 #pragma unroll
-  for (int k = 0; k < G / 4; ++k) decode4(w[k], s, o + 4 * k);
-  if (kOff) {
-    const int cut = kBlock - (at & (kBlock - 1));
-    if (cut < G) {  // the group crosses into the next block
-      const Scale t = scale_of(heads[(at >> 7) + 2]);
-      masked |= t.masked;
+    for (int k = 0; k < G / 4; ++k) decode4(w[k], s, o + 4 * k);
+    if (kOff && cut < G) {
       float y[G];
 #pragma unroll
       for (int k = 0; k < G / 4; ++k) decode4(w[k], t, y + 4 * k);
 #pragma unroll
       for (int k = 0; k < G; ++k)
         if (k >= cut) o[k] = y[k];
+    }
+  } else {
+    float s0, f0, s1, f1;
+    plain_scale(h0, s0, f0);
+    if (kOff) plain_scale(h1, s1, f1);
+#pragma unroll
+    for (int k = 0; k < G; k += 2) {
+      const uint32_t x = w[k / 4];
+      const float m0 = (k & 2) ? magic_byte<2>(x) : magic_byte<0>(x);
+      const float m1 = (k & 2) ? magic_byte<3>(x) : magic_byte<1>(x);
+      if (kOff) {
+        o[k] = fmaf(m0, k < cut ? s0 : s1, k < cut ? f0 : f1);
+        o[k + 1] = fmaf(m1, k + 1 < cut ? s0 : s1, k + 1 < cut ? f0 : f1);
+      } else {
+        upk(fma2(pk(m0, m1), splat(s0), splat(f0)), o[k], o[k + 1]);
+      }
     }
   }
 }
@@ -245,57 +316,77 @@ __device__ __forceinline__ float quant_at(const RowPtr& rp, int64_t j) {
     return Type<QT>::load(rp.quant + j * Quant<QT>::kBytes);
 }
 
-// A lane's column of group g of step v of a chunk, from the chunk's start.
+// A lane's column of its group g in a chunk, from the chunk's start.
 template <int QT>
-__device__ __forceinline__ int group_col(int v, int g, int lane) {
-  return ((v * Quant<QT>::kGroups + g) * 32 + lane) * Quant<QT>::kGroup;
+__device__ __forceinline__ int group_col(int g, int lane) {
+  return (g * 32 + lane) * Quant<QT>::kGroup;
 }
 
-// The 8 columns of step v (0 or 1) of a chunk: values of both operands.
-// whole: every column of the chunk lies inside the row. Groups that cross
-// the row's ends are read element by element, -inf outside.
+// A lane's 16 columns of a chunk that lies inside the row: base values, and
+// quant values (packed ones for the 16-bit types), wrong where a block is
+// special (bit 8 of the result).
 template <int QT, bool kOff>
-__device__ __forceinline__ void step_values(const RowPtr& rp, int64_t V, int64_t c,
-                                            const unsigned char* slot, int v, int lane, bool whole,
-                                            bool& masked, float* b, float* q) {
+__device__ __forceinline__ uint32_t step_plain(int off, const unsigned char* slot, int lane,
+                                               float* b, float* q, uint32_t* qw) {
   constexpr int G = Quant<QT>::kGroup;
-  const int off = kOff ? rp.off : 0;
+  uint32_t special = 0u;
 #pragma unroll
   for (int g = 0; g < Quant<QT>::kGroups; ++g) {
-    const int at = group_col<QT>(v, g, lane) - off;
-    const int64_t j = c * kChunk + at;
+    const int at = group_col<QT>(g, lane) - (kOff ? off : 0);
+    slot_values<G, kOff, false>(slot, reinterpret_cast<const uint32_t*>(slot + Slot<QT>::kHeads),
+                                at, special, b + g * G);
+    const unsigned char* qs = slot + Slot<QT>::kQuant;
+    if constexpr (QT == kFromPack) {
+      slot_values<G, kOff, false>(qs, reinterpret_cast<const uint32_t*>(qs + kCodeBytes), at,
+                                  special, q + g * G);
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(qs + group_col<QT>(g, lane) * Quant<QT>::kBytes);
+      if constexpr (QT == KLD_F32) {
+        q[4 * g] = __uint_as_float(w.x);
+        q[4 * g + 1] = __uint_as_float(w.y);
+        q[4 * g + 2] = __uint_as_float(w.z);
+        q[4 * g + 3] = __uint_as_float(w.w);
+      } else {
+        qw[4 * g] = w.x;
+        qw[4 * g + 1] = w.y;
+        qw[4 * g + 2] = w.z;
+        qw[4 * g + 3] = w.w;
+      }
+    }
+  }
+  return special;
+}
+
+// The same for any chunk, quant values unpacked: masks and bad blocks read as
+// such, groups that cross the row's ends element by element, -inf outside.
+template <int QT, bool kOff>
+__device__ __forceinline__ void step_general(const RowPtr& rp, int64_t V, int c,
+                                             const unsigned char* slot, int lane, float* b,
+                                             float* q) {
+  constexpr int G = Quant<QT>::kGroup;
+  const int off = kOff ? rp.off : 0;
+  uint32_t special = 0u;
+#pragma unroll
+  for (int g = 0; g < Quant<QT>::kGroups; ++g) {
+    const int at = group_col<QT>(g, lane) - off;
+    const int64_t j = static_cast<int64_t>(c) * kChunk + at;
     float* bg = b + g * G;
     float* qg = q + g * G;
-    if (whole || (j >= 0 && j + G <= V)) {
-      slot_values<G, kOff>(slot, reinterpret_cast<const uint32_t*>(slot + Slot<QT>::kHeads), at,
-                           masked, bg);
+    if (j >= 0 && j + G <= V) {
+      slot_values<G, kOff, true>(slot, reinterpret_cast<const uint32_t*>(slot + Slot<QT>::kHeads),
+                                 at, special, bg);
       const unsigned char* qs = slot + Slot<QT>::kQuant;
       if constexpr (QT == kFromPack) {
-        slot_values<G, kOff>(qs, reinterpret_cast<const uint32_t*>(qs + kCodeBytes), at, masked, qg);
+        slot_values<G, kOff, true>(qs, reinterpret_cast<const uint32_t*>(qs + kCodeBytes), at,
+                                   special, qg);
       } else {
         const uint4 w = *reinterpret_cast<const uint4*>(qs + (at + off) * Quant<QT>::kBytes);
-        if constexpr (QT == KLD_F32) {
-          qg[0] = __uint_as_float(w.x);
-          qg[1] = __uint_as_float(w.y);
-          qg[2] = __uint_as_float(w.z);
-          qg[3] = __uint_as_float(w.w);
-        } else {
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (QT == KLD_BF16) {
-              qg[2 * k] = __uint_as_float(ww[k] << 16);
-              qg[2 * k + 1] = __uint_as_float(ww[k] & 0xffff0000u);
-            } else {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[k]));
-              qg[2 * k] = f.x;
-              qg[2 * k + 1] = f.y;
-            }
-          }
-        }
+        for (int k = 0; k < G; ++k)
+          qg[k] = QT == KLD_F32 ? __uint_as_float(ww[k & 3]) : q_el<kPacked16<QT>>(nullptr, ww, k);
       }
     } else {
-      masked = true;
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         const bool in = j + k >= 0 && j + k < V;
@@ -339,36 +430,37 @@ struct Shared {
   uint32_t flags;
 };
 
-// The frame and centre of a warp (uniform).
-struct Frame {
-  float F, K, T;  // T: a value above it moves them
+// What a lane keeps of its part of the row: its warp's frame and centre
+// (uniform), its sums (Part), its maxima and the first chunks they are in.
+struct State {
+  float F, K, T;  // T: a value above it moves the frame and the centre
   int form;       // order of the log-ratio's roundings (ratio_form)
-};
-// A lane's sums (Part), the polynomial steps' as pairs of fp32.
-struct Sums {
-  f2 S, A, C;
-  float D, E, Q;
+  float S, A, C, D, E, Q;
+  float mb, mq;
+  int ib, iq;
 };
 
-// Moves a warp's frame to its lanes' maximum um of the step (b, q), rebasing
+// Moves a warp's frame to its step's maximum M (um: the lane's own), rebasing
 // the lanes' sums exactly in F and by
 //   A' = A + d S,  C' = e^d C + (e^d - 1) A + (e^d - 1 - d) S,
 //   E' = E + d D,  Q' = e^d Q
 // in K (d its change).
-__device__ __forceinline__ void raise(Frame& f, Sums& s, const float* b, const float* q, float um,
-                                   float M) {
+template <int QT>
+__device__ __forceinline__ void raise(State& s, const float* b, const float* q, const uint32_t* qw,
+                                      float um, float M) {
   float qm = 0.f;
 #pragma unroll
-  for (int k = 7; k >= 0; --k)
-    if (b[k] == M) qm = q[k];
+  for (int k = 15; k >= 0; --k)
+    if (b[k] == M) qm = q_el<kPacked16<QT>>(q, qw, k);
   const unsigned who = __ballot_sync(0xffffffffu, um == M);
   qm = __shfl_sync(0xffffffffu, qm, __ffs(static_cast<int>(who)) - 1);
-  const float K = fabsf(qm) < INFINITY ? M - qm : f.K;  // a masked or NaN quant entry sets none
+  const float K = fabsf(qm) < INFINITY ? M - qm : s.K;  // a masked or NaN quant entry sets none
   const float F = floorf(M * kLog2e);
-  if (f.F != kNoFrame) {
-    const float sc = static_cast<float>(pow2i(f.F - F));
-    const float d = K - f.K;
-    const float ld = static_cast<float>(kLambda) * d;
+  if (s.F != kNoFrame) {
+    const float sc = static_cast<float>(pow2d(s.F - F));
+    const float d = K - s.K;
+    const float lam = static_cast<float>(kLambda);
+    const float ld = lam * d;
     float e1, phi;  // e^ld - 1, e^ld - 1 - ld
     if (fabsf(d) <= kTau) {
       phi = d * d * phi_q(d);
@@ -377,94 +469,129 @@ __device__ __forceinline__ void raise(Frame& f, Sums& s, const float* b, const f
       e1 = ex2(d * kLog2e) - 1.f;
       phi = e1 - ld;
     }
-    const float lam = static_cast<float>(kLambda);
-    float s0[2], a0[2], c0[2];
-    upk(s.S, s0[0], s0[1]);
-    upk(s.A, a0[0], a0[1]);
-    upk(s.C, c0[0], c0[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      c0[k] = sc * (c0[k] + e1 * c0[k] + e1 * lam * a0[k] + phi * s0[k]);
-      a0[k] = sc * (a0[k] + d * s0[k]);
-      s0[k] = sc * s0[k];
-    }
-    s.S = pk(s0[0], s0[1]);
-    s.A = pk(a0[0], a0[1]);
-    s.C = pk(c0[0], c0[1]);
+    s.C = sc * (s.C + e1 * s.C + e1 * lam * s.A + phi * s.S);
+    s.A = sc * (s.A + d * s.S);
+    s.S *= sc;
     s.E = sc * (s.E + d * s.D);
     s.D *= sc;
     s.Q = sc * (s.Q + e1 * s.Q);
   }
-  f.F = F;
-  f.K = K;
-  f.T = M + kRaiseMargin;
-  f.form = ratio_form(M, K);
+  s.F = F;
+  s.K = K;
+  s.T = M + kRaiseMargin;
+  s.form = ratio_form(M, K);
 }
 
+// S += e, A += e x, C += e (e^x - 1 - x) with tier T's polynomial.
 template <int T>
-__device__ __forceinline__ void add_poly(Sums& s, const Frame& f, const float* b, const f2* x) {
-  const f2 L2 = splat(kLog2e), nf = splat(-f.F);
+__device__ __forceinline__ void add_poly(State& s, const float* b, const f2* x) {
+  const f2 L2 = splat(kLog2e), nf = splat(-s.F);
+  // Two accumulator sets halve the dependent-add chains.
+  f2 S[2] = {splat(0.f), splat(0.f)}, A[2] = {splat(0.f), splat(0.f)}, C[2] = {splat(0.f), splat(0.f)};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 8; ++k) {
     float u0, u1;
     upk(fma2(pk(b[2 * k], b[2 * k + 1]), L2, nf), u0, u1);
     const f2 e = pk(ex2(u0), ex2(u1));
     const f2 t = mul2(e, x[k]);
-    s.S = add2(s.S, e);
-    s.A = add2(s.A, t);
-    s.C = fma2(mul2(t, x[k]), phi_q2<T>(x[k]), s.C);
+    S[k & 1] = add2(S[k & 1], e);
+    A[k & 1] = add2(A[k & 1], t);
+    C[k & 1] = fma2(mul2(t, x[k]), phi_q2<T>(x[k]), C[k & 1]);
   }
+  float v0, v1;
+  upk(add2(S[0], S[1]), v0, v1);
+  s.S += v0 + v1;
+  upk(add2(A[0], A[1]), v0, v1);
+  s.A += v0 + v1;
+  upk(add2(C[0], C[1]), v0, v1);
+  s.C += v0 + v1;
 }
-// Large or non-finite log-ratios. A masked base entry has e = 0 and gives its
-// h to Q; x = -inf with a base entry above -inf makes E non-finite, which
-// sends the row to slow_row.
-__device__ __forceinline__ void add_direct(Sums& s, const Frame& f, const float* b, const float* q) {
+
+// Adds a chunk's 16 columns of a lane (the whole warp together) to its
+// state. Entries whose bit in `valid` is 0 are -inf in both operands (masks,
+// columns outside the row): they have weight 0 and take x = 0. i: the
+// warp's number of the chunk.
+template <int QT>
+__device__ __forceinline__ void add_step(State& s, const float* b, const float* q,
+                                         const uint32_t* qw, unsigned valid, int i) {
+  constexpr int kPk = kPacked16<QT>;
+  const float mb = tree_max<16, false>(b);
+  float mq;
+  if constexpr (kPk != 0) {
+    uint32_t m2 = qw[0];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float e = ex2(fmaf(b[k], kLog2e, -f.F));
-    const float qk = q[k] + f.K;
-    const float x = f.form == 2 ? q[k] - (b[k] - f.K) : (f.form == 1 ? qk - b[k] : (q[k] - b[k]) + f.K);
-    s.D += e;
-    s.E += b[k] == neg_inf() ? 0.f : e * x;
-    s.Q += ex2(fmaf(qk, kLog2e, -f.F));
+    for (int w = 1; w < 8; ++w) m2 = Packed<kPk>::max2(m2, qw[w]);
+    mq = fmaxf(Packed<kPk>::lo(m2), Packed<kPk>::hi(m2));
+  } else {
+    mq = tree_max<16, false>(q);
+  }
+  if (__any_sync(0xffffffffu, mb > s.T)) raise<QT>(s, b, q, qw, mb, warp_max(mb));
+  f2 x[8];
+  float ax;
+  if (s.form == 0) {
+    ax = log_ratios<16, 0, kPk>(b, q, valid, s.K, x, qw);
+  } else {
+    float y[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y[k] = q_el<kPk>(q, qw, k);
+    ax = s.form == 1 ? log_ratios<16, 1>(b, y, valid, s.K, x) : log_ratios<16, 2>(b, y, valid, s.K, x);
+  }
+  if (__all_sync(0xffffffffu, ax <= kTauA)) {
+    add_poly<0>(s, b, x);
+  } else if (__all_sync(0xffffffffu, ax <= kTauB)) {
+    add_poly<1>(s, b, x);
+  } else if (__all_sync(0xffffffffu, ax <= kTau)) {
+    add_poly<2>(s, b, x);
+  } else {
+    // Large or non-finite log-ratios. A masked base entry has e = 0 and gives
+    // its h to Q; x = -inf with a base entry above -inf makes E non-finite,
+    // which sends the row to slow_row.
+    float D = 0.f, E = 0.f, Q = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float xs[2];
+      upk(x[k], xs[0], xs[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float bk = b[2 * k + h];
+        const float e = ex2(fmaf(bk, kLog2e, -s.F));
+        D += e;
+        E += bk == neg_inf() ? 0.f : e * xs[h];
+        Q += ex2(fmaf(q_el<kPk>(q, qw, 2 * k + h) + s.K, kLog2e, -s.F));
+      }
+    }
+    s.D += D;
+    s.E += E;
+    s.Q += Q;
+  }
+  if (mb > s.mb) {
+    s.mb = mb;
+    s.ib = i;
+  }
+  if (mq > s.mq) {
+    s.mq = mq;
+    s.iq = i;
   }
 }
 
-// Adds a step's 8 columns to a lane's sums (the whole warp together).
-// masked: some lane may hold -inf; entries that are -inf in both operands
-// (masks, columns outside the row) have weight 0 and take x = 0.
-__device__ __forceinline__ void accumulate(Sums& s, Frame& f, const float* b, const float* q,
-                                           float um, bool masked) {
-  const bool up = um > f.T;
-  if (__any_sync(0xffffffffu, up)) raise(f, s, b, q, um, warp_max(um));
-  f2 x[4];
-  float ax;
-  if (__any_sync(0xffffffffu, masked)) {
-    ax = 0.f;
+// add_step for a chunk that crosses the row's ends or holds masked or bad
+// blocks. By value, so that the caller's state stays in registers.
+template <int QT, bool kOff>
+__device__ __noinline__ State add_general(State s, const RowPtr rp, int64_t V, int c,
+                                          const unsigned char* slot, int lane, int i) {
+  float b[16], q[16];
+  uint32_t qw[8];
+  step_general<QT, kOff>(rp, V, c, slot, lane, b, q);
+  unsigned valid = 0u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float y[2];
+  for (int k = 0; k < 16; ++k)
+    if (b[k] != neg_inf() || q[k] != neg_inf()) valid |= 1u << k;
+  if constexpr (kPacked16<QT> != 0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float bk = b[2 * k + i], qk = q[2 * k + i];
-        y[i] = f.form == 2 ? qk - (bk - f.K) : (f.form == 1 ? (qk + f.K) - bk : (qk - bk) + f.K);
-        if (bk == neg_inf() && qk == neg_inf()) y[i] = 0.f;
-      }
-      ax = max3_nan(ax, fabsf(y[0]), fabsf(y[1]));
-      x[k] = pk(y[0], y[1]);
-    }
-  } else if (f.form == 0)
-    ax = log_ratios<8, 0>(b, q, 0xffu, f.K, x);
-  else if (f.form == 1)
-    ax = log_ratios<8, 1>(b, q, 0xffu, f.K, x);
-  else
-    ax = log_ratios<8, 2>(b, q, 0xffu, f.K, x);
-  if (__all_sync(0xffffffffu, ax <= kTauA))
-    add_poly<0>(s, f, b, x);
-  else if (__all_sync(0xffffffffu, ax <= kTau))
-    add_poly<2>(s, f, b, x);
-  else
-    add_direct(s, f, b, q);
+    for (int k = 0; k < 8; ++k) qw[k] = pack16<QT>(q[2 * k], q[2 * k + 1]);
+  }
+  add_step<QT>(s, b, q, qw, valid, i);
+  return s;
 }
 
 // The parts of a row merged by one warp, in fp64, to the largest frame and
@@ -489,7 +616,7 @@ __device__ __noinline__ void merge(Shared& sh, int parts, float scale) {
   for (int i = lane; i < parts; i += 32) {
     const Part p = sh.part[i];
     if (p.S == 0.f && p.D == 0.f && p.E == 0.f && p.Q == 0.f) continue;
-    const double sc = pow2i(p.F - F);
+    const double sc = pow2d(p.F - F);
     const double d = static_cast<double>(K) - static_cast<double>(p.K);
     double e1 = 0.0, phi = 0.0;
     if (d != 0.0) {
@@ -657,12 +784,45 @@ __device__ void write_row(const Operands& in, const Outputs& out, const RowPtr& 
   if (out.amax_q) out.amax_q[r] = rec.argmax_quant;
 }
 
+// A lane's 16 gradient values of the chunk that starts at column j0 of the
+// row's grid. check: the chunk may cross the row's ends.
+template <int QT, int OT>
+__device__ __forceinline__ void store_grad(char* grow, int64_t j0, int64_t V, int lane, bool check,
+                                           const float* x) {
+  constexpr int G = Quant<QT>::kGroup;
+  constexpr int OE = 16 / Type<OT>::kBytes;  // elements of an output vector
+  // All of a row's groups lie alike on the 16-byte grid of the output.
+  char* at = grow + (j0 + lane * G) * Type<OT>::kBytes;
+  const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+#pragma unroll
+  for (int g = 0; g < Quant<QT>::kGroups; ++g) {
+    char* dst = at + g * 32 * G * Type<OT>::kBytes;
+    const float* y = x + g * G;
+    const int64_t j = j0 + group_col<QT>(g, lane);
+    if ((!check || (j >= 0 && j + G <= V)) && (OE <= G ? mis == 0u : (mis & 7u) == 0u)) {
+      if (OE <= G) {
+#pragma unroll
+        for (int k = 0; k < G; k += OE)
+          __stcs(reinterpret_cast<uint4*>(dst + k * Type<OT>::kBytes), Type<OT>::vec(y + k));
+      } else {
+        const float z[8] = {y[0], y[1], y[2], y[3], 0.f, 0.f, 0.f, 0.f};
+        const uint4 w = Type<OT>::vec(z);
+        __stcs(reinterpret_cast<uint2*>(dst), make_uint2(w.x, w.y));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < G; ++k)
+        if (j + k >= 0 && j + k < V) Type<OT>::store(dst + k * Type<OT>::kBytes, y[k]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 
 // grid = N * C CTAs, clusters of C = gridDim / N; slots: shared-memory slots
 // per warp (>= kDepth).
 template <int QT, int OT, bool kOff>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     kld_packed_rows_kernel(const Operands in, const Outputs out, int C, int slots) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared sh;
@@ -689,60 +849,58 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int off = kOff ? rp.off : 0;
 
   // This CTA's chunks [c0, c1); warp w takes c0 + w + i * kWarps, i < n.
-  const int64_t chunks = (V + off + kChunk - 1) / kChunk;
-  const int64_t c0 = chunks * rank / C, c1 = chunks * (rank + 1) / C;
-  const int n = c0 + warp < c1 ? static_cast<int>((c1 - c0 - warp + kWarps - 1) / kWarps) : 0;
+  const int chunks = static_cast<int>((V + off + kChunk - 1) / kChunk);
+  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * rank / C);
+  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (rank + 1) / C);
+  const int n = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+  // Chunks [in0, in1) lie inside the row (their vectors whole, their headers
+  // and shifted codes in the row's buffers).
+  const int in0 = kOff ? 1 : 0;
+  const int in1 = static_cast<int>((V + off) / kChunk);
+  const LanePtr lp = lane_ptr<QT, kOff>(rp, lane);
   unsigned char* my = ring + static_cast<size_t>(warp) * slots * Slot<QT>::kBytes;
   const uint32_t my32 = smem_u32(my);
-  const int64_t first = c0 + warp;
+  const int first = c0 + warp;
+  auto inner = [&](int c) { return c >= in0 && c < in1; };
+  auto load = [&](int i, int slot) {
+    const int c = first + i * kWarps;
+    fetch<QT, kOff>(lp, rp, V, nb, c, inner(c), my32 + slot * Slot<QT>::kBytes, lane);
+  };
 
-  Sums sum;
-  sum.S = sum.A = sum.C = splat(0.f);
-  sum.D = sum.E = sum.Q = 0.f;
-  Frame fr;
-  fr.F = kNoFrame;
-  fr.K = 0.f;
-  fr.T = neg_inf();
-  fr.form = 0;
-  float mb = neg_inf(), mq = neg_inf();  // this lane's maxima and the first chunks they are in
-  int ib = 0, iq = 0;
+  State st;
+  st.F = kNoFrame;
+  st.K = 0.f;
+  st.T = neg_inf();
+  st.form = 0;
+  st.S = st.A = st.C = st.D = st.E = st.Q = 0.f;
+  st.mb = st.mq = neg_inf();
+  st.ib = st.iq = 0;
 
   // ---- sums
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) {
-    if (i < n) fetch<QT, kOff>(rp, V, nb, first + i * kWarps, my32 + i * Slot<QT>::kBytes, lane);
+    if (i < n) load(i, i);
     copy_commit();
   }
   int cur = 0, nxt = kDepth == slots ? 0 : kDepth;  // slots of chunks i and i + kDepth
   for (int i = 0; i < n; ++i) {
     copy_wait<kDepth - 1>();
     __syncwarp();
-    const int64_t c = first + static_cast<int64_t>(i) * kWarps;
+    const int c = first + i * kWarps;
     const unsigned char* slot = my + cur * Slot<QT>::kBytes;
-    const bool whole = (!kOff || c > 0 || off == 0) && c * kChunk - off + kChunk <= V;
-    float cb = neg_inf(), cq = neg_inf();
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float b[8], q[8];
-      bool masked = false;
-      step_values<QT, kOff>(rp, V, c, slot, v, lane, whole, masked, b, q);
-      const float umb = max8(b), umq = max8(q);
-      cb = fmaxf(cb, umb);
-      cq = fmaxf(cq, umq);
-      accumulate(sum, fr, b, q, umb, masked);
+    bool general = !inner(c);
+    float b[16], q[16];
+    uint32_t qw[8];
+    if (!general) {
+      const uint32_t special = step_plain<QT, kOff>(off, slot, lane, b, q, qw);
+      general = __any_sync(0xffffffffu, (special & 256u) != 0u);
     }
-    if (cb > mb) {
-      mb = cb;
-      ib = i;
-    }
-    if (cq > mq) {
-      mq = cq;
-      iq = i;
-    }
+    if (!general)
+      add_step<QT>(st, b, q, qw, 0xffffu, i);
+    else
+      st = add_general<QT, kOff>(st, rp, V, c, slot, lane, i);
     __syncwarp();
-    if (i + kDepth < n)
-      fetch<QT, kOff>(rp, V, nb, first + static_cast<int64_t>(i + kDepth) * kWarps,
-                      my32 + nxt * Slot<QT>::kBytes, lane);
+    if (i + kDepth < n) load(i + kDepth, nxt);
     copy_commit();
     if (++cur == slots) cur = 0;
     if (++nxt == slots) nxt = 0;
@@ -750,21 +908,17 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   // ---- merge: lanes, then every warp of the cluster
   {
-    float s0, s1;
     Part w;
-    w.F = fr.F;
-    w.K = fr.K;
-    upk(sum.S, s0, s1);
-    w.S = sum_lanes(s0 + s1);
-    upk(sum.A, s0, s1);
-    w.A = sum_lanes(s0 + s1);
-    upk(sum.C, s0, s1);
-    w.C = sum_lanes(s0 + s1);
-    w.D = sum_lanes(sum.D);
-    w.E = sum_lanes(sum.E);
-    w.Q = sum_lanes(sum.Q);
-    w.mb = warp_max(mb);
-    w.mq = warp_max(mq);
+    w.F = st.F;
+    w.K = st.K;
+    w.S = sum_lanes(st.S);
+    w.A = sum_lanes(st.A);
+    w.C = sum_lanes(st.C);
+    w.D = sum_lanes(st.D);
+    w.E = sum_lanes(st.E);
+    w.Q = sum_lanes(st.Q);
+    w.mb = warp_max(st.mb);
+    w.mq = warp_max(st.mq);
     if (C > 1) cluster_wait();  // every CTA of the cluster has started
     if (lane < C) {             // lane k leaves the part with CTA k
       const uint32_t* words = reinterpret_cast<const uint32_t*>(&w);
@@ -789,14 +943,13 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncthreads();
   // Lowest columns of the row's maxima: the lanes that hold one look through
   // the first chunk in which it appeared; rank 0 collects.
-  if (n > 0 && (mb == sh.total.mb || mq == sh.total.mq)) {
+  if (n > 0 && (st.mb == sh.total.mb || st.mq == sh.total.mq)) {
     for (int which = 0; which < 2; ++which) {
       const float m = which ? sh.total.mq : sh.total.mb;
-      if ((which ? mq : mb) != m) continue;
-      const int64_t c = first + static_cast<int64_t>(which ? iq : ib) * kWarps;
+      if ((which ? st.mq : st.mb) != m) continue;
+      const int64_t c = first + (which ? st.iq : st.ib) * kWarps;
       for (int k = 0; k < 16; ++k) {
-        const int at = group_col<QT>(k >> 3, (k & 7) / Quant<QT>::kGroup, lane) +
-                       (k & 7) % Quant<QT>::kGroup - off;
+        const int at = group_col<QT>(k / Quant<QT>::kGroup, lane) + k % Quant<QT>::kGroup - off;
         const int64_t j = c * kChunk + at;
         if (j < 0 || j >= V) continue;
         if ((which ? quant_at<QT>(rp, j) : base_at<QT>(rp, j)) == m) {
@@ -814,7 +967,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     Slow s;
     slow_row<QT>(sh, rp, V, s);
     if (grow) {
-      const int64_t j0 = c0 * kChunk - off, j1 = c1 * kChunk - off;
+      const int64_t j0 = static_cast<int64_t>(c0) * kChunk - off;
+      const int64_t j1 = static_cast<int64_t>(c1) * kChunk - off;
       slow_grad<QT, OT>(rp, j0 < 0 ? 0 : j0, j1 < V ? j1 : V, s, grow, out.scale);
     }
     if (C > 1) {
@@ -837,53 +991,35 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = n - 1; i >= 0; --i) {
       copy_wait<kDepth - 1>();
       __syncwarp();
-      const int64_t c = first + static_cast<int64_t>(i) * kWarps;
+      const int c = first + i * kWarps;
       const unsigned char* slot = my + cur * Slot<QT>::kBytes;
-      const bool whole = (!kOff || c > 0 || off == 0) && c * kChunk - off + kChunk <= V;
+      bool general = !inner(c);
+      float b[16], q[16];
+      uint32_t qw[8];
+      if (!general) {
+        const uint32_t special = step_plain<QT, kOff>(off, slot, lane, b, q, qw);
+        general = __any_sync(0xffffffffu, (special & 256u) != 0u);
+        if constexpr (kPacked16<QT> != 0) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        float b[8], q[8];
-        bool masked = false;
-        step_values<QT, kOff>(rp, V, c, slot, v, lane, whole, masked, b, q);
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          float u0, u1, v0, v1;
-          upk(fma2(pk(b[k], b[k + 1]), L2, fb), u0, u1);
-          upk(fma2(pk(q[k], q[k + 1]), L2, fq), v0, v1);
-          // Products rounded apart, so equal rows give exactly zero: as FMAs
-          // with zero, since a packed product may be joined with the
-          // difference into one FMA (measured: 2.5e-8 p instead of 0).
-          const f2 pr = fma2(pk(ex2(u0), ex2(u1)), cb2, zero2);
-          const f2 rr = fma2(pk(ex2(v0), ex2(v1)), cq2, zero2);
-          upk(sub2(rr, pr), b[k], b[k + 1]);
-        }
-        constexpr int G = Quant<QT>::kGroup;
-        constexpr int OE = 16 / Type<OT>::kBytes;  // elements of an output vector
-#pragma unroll
-        for (int g = 0; g < Quant<QT>::kGroups; ++g) {
-          const int64_t j = c * kChunk + group_col<QT>(v, g, lane) - off;
-          char* dst = grow + j * Type<OT>::kBytes;
-          const float* x = b + g * G;
-          const bool in_row = whole || (j >= 0 && j + G <= V);
-          if (in_row && OE <= G && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-#pragma unroll
-            for (int k = 0; k < G; k += OE)
-              __stcs(reinterpret_cast<uint4*>(dst + k * Type<OT>::kBytes), Type<OT>::vec(x + k));
-          } else if (in_row && OE == 8 && G == 4 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
-            const float y[8] = {x[0], x[1], x[2], x[3], 0.f, 0.f, 0.f, 0.f};
-            const uint4 w = Type<OT>::vec(y);
-            __stcs(reinterpret_cast<uint2*>(dst), make_uint2(w.x, w.y));
-          } else {
-#pragma unroll
-            for (int k = 0; k < G; ++k)
-              if (j + k >= 0 && j + k < V) Type<OT>::store(dst + k * Type<OT>::kBytes, x[k]);
-          }
+          for (int k = 0; k < 16; ++k) q[k] = q_el<kPacked16<QT>>(nullptr, qw, k);
         }
       }
+      if (general) step_general<QT, kOff>(rp, V, c, slot, lane, b, q);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float u0, u1, v0, v1;
+        upk(fma2(pk(b[k], b[k + 1]), L2, fb), u0, u1);
+        upk(fma2(pk(q[k], q[k + 1]), L2, fq), v0, v1);
+        // Products rounded apart, so equal rows give exactly zero: as FMAs
+        // with zero, since a packed product may be joined with the
+        // difference into one FMA (measured: 2.5e-8 p instead of 0).
+        const f2 pr = fma2(pk(ex2(u0), ex2(u1)), cb2, zero2);
+        const f2 rr = fma2(pk(ex2(v0), ex2(v1)), cq2, zero2);
+        upk(sub2(rr, pr), b[k], b[k + 1]);
+      }
+      store_grad<QT, OT>(grow, static_cast<int64_t>(c) * kChunk - off, V, lane, general, b);
       __syncwarp();
-      if (i - slots >= 0)
-        fetch<QT, kOff>(rp, V, nb, first + static_cast<int64_t>(i - slots) * kWarps,
-                        my32 + cur * Slot<QT>::kBytes, lane);
+      if (i - slots >= 0) load(i - slots, cur);
       copy_commit();
       if (--cur < 0) cur = slots - 1;
     }
@@ -916,12 +1052,15 @@ struct Shape {
 };
 template <int QT>
 Shape shape_for(int64_t N, int64_t V, int sm_count) {
-  const int most = 74 * 1024 / (kWarps * Slot<QT>::kBytes);  // three CTAs an SM
-  const int64_t per_warp = (V + kChunk - 1) / kChunk / kWarps + 1;
+  // Shared memory of kCtasPerSm CTAs an SM.
+  const int most = 44 * 1024 / (kWarps * Slot<QT>::kBytes);
+  const int64_t chunks = (V + kChunk - 1) / kChunk + 1;
+  // Few rows are split until the CTAs fill the SMs (or a warp has one chunk).
   int c = 1;
-  while (c < kMaxCluster && (per_warp + c - 1) / c > most) c *= 2;
-  while (c < kMaxCluster && N * c * 2 <= sm_count * 2 && (per_warp + c - 1) / c > 1) c *= 2;
-  int64_t s = (per_warp + c - 1) / c + 1;
+  while (c < kMaxCluster && N * c < static_cast<int64_t>(sm_count) * kCtasPerSm &&
+         chunks > static_cast<int64_t>(c) * kWarps)
+    c *= 2;
+  int64_t s = (chunks + c * kWarps - 1) / (c * kWarps) + 1;
   if (s > most) s = most;
   if (s < kDepth) s = kDepth;
   return {c, static_cast<int>(s)};
