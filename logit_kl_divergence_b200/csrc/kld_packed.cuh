@@ -61,10 +61,13 @@ __device__ __forceinline__ void plain_scale(uint32_t head, float& step, float& o
   const float b = __uint_as_float(0x4b400000u + static_cast<uint32_t>(static_cast<int32_t>(head) >> 9));
   off = (b - 20971520.f) * step;  // base - 2^23, exactly
 }
-// Byte k of w as the float 2^23 + byte.
+// Byte k of w as the float 2^23 + byte, in one byte permute (written out:
+// the compiler's own choice took 1.5 to 2 instructions).
 template <int K>
 __device__ __forceinline__ float magic_byte(uint32_t w) {
-  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 + K));
+  uint32_t y;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(y) : "r"(w), "r"(0x4b000000u), "n"(0x7650 + K));
+  return __uint_as_float(y);
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
