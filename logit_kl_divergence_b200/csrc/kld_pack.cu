@@ -48,7 +48,8 @@ struct Steps {
 // Units of a lane in a group, 32 apart, loaded together. Measured at 2048
 // rows: fp32 rows of 151936 253 us with two, 266 with one; shifted bf16 rows
 // of 131073 184 us with one, 192 with two; four spill or halve the CTAs.
-constexpr int pack_units(bool aligned) { return aligned ? 2 : 1; }
+template <bool kAligned>
+constexpr int kPackUnits = kAligned ? 2 : 1;
 constexpr int kUnpackUnits = 4;  // bf16 checkpoint to fp32 316 us, one by one 370 us
 
 // 16 elements of a row from column j on. Full units whose 16-byte vectors
@@ -179,8 +180,7 @@ __global__ void __launch_bounds__(kThreads)
                     uint8_t* __restrict__ codes, uint32_t* __restrict__ heads) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t upr = static_cast<uint32_t>(nb * kLanes);  // units per row
-  constexpr int kPackUnits = pack_units(kAligned);
-  const uint32_t per = (upr + 32 * kPackUnits - 1) / (32 * kPackUnits);
+  const uint32_t per = (upr + 32 * kPackUnits<kAligned> - 1) / (32 * kPackUnits<kAligned>);
   const char* begin = static_cast<const char*>(logits);
   const char* end = begin + N * V * Type<DT>::kBytes;
   constexpr int kWarps = kThreads / 32;
@@ -188,14 +188,14 @@ __global__ void __launch_bounds__(kThreads)
   for (Steps at(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), per); at.row < N;
        at.add(stride, per)) {
     const char* row = begin + at.row * V * Type<DT>::kBytes;
-    const uint32_t u0 = at.group * (32 * kPackUnits) + lane;
-    float x[kPackUnits][kUnit];
+    const uint32_t u0 = at.group * (32 * kPackUnits<kAligned>) + lane;
+    float x[kPackUnits<kAligned>][kUnit];
 #pragma unroll
-    for (int i = 0; i < kPackUnits; ++i)
+    for (int i = 0; i < kPackUnits<kAligned>; ++i)
       if (u0 + 32 * i < upr)
         load_unit<DT, kAligned>(row, static_cast<int64_t>(u0 + 32 * i) * kUnit, V, begin, end, x[i]);
 #pragma unroll
-    for (int i = 0; i < kPackUnits; ++i) {
+    for (int i = 0; i < kPackUnits<kAligned>; ++i) {
       const uint32_t u = u0 + 32 * i;
       uint32_t head;
       uint4 c;
@@ -311,7 +311,7 @@ cudaError_t pack_typed(const void* logits, int64_t N, int64_t V, uint8_t* codes,
   const int64_t nb = (V + kBlock - 1) / kBlock;
   const bool aligned = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 &&
                        (N == 1 || V * Type<DT>::kBytes % 16 == 0);
-  const int64_t group = 32 * pack_units(aligned);
+  const int64_t group = 32 * (aligned ? kPackUnits<true> : kPackUnits<false>);
   const int grid = blocks_for(N * ((nb * kLanes + group - 1) / group), sm_count);
   if (aligned)
     kld_pack_kernel<DT, true><<<grid, kThreads, 0, s>>>(logits, N, V, nb, codes, heads);
