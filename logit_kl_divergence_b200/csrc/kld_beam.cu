@@ -13,15 +13,18 @@
 // merges lse in fp64, scores the kept entries in fp64 and sorts the best k.
 //
 // What can still be among the k largest: any k entries give a bound, since
-// at least k are >= the least of them. The CTA takes its first tile's lane
-// maxima, of each warp the ceil(k / warps)-th largest, and the least of
-// those: a few shuffles, and only some 1-2 % of a tile lies above. Entries
-// at or above the bound go to a list in shared memory, thinned once more in
-// the same way at the end. Should the list overflow (large ties, rising
-// rows) the part is done again 256 columns at a time with exact pruning.
+// at least k are >= the least of them. The CTA takes its lanes'
+// maxima, of each warp the few largest, and the k-th largest of those: close
+// to the k-th largest of the tiles so far. The bound is renewed after 1, 2,
+// 4, ... tiles, so that about k entries pass it from one time to the next.
+// They go to a list in shared memory. Should the list overflow
+// (large ties, rising rows) the part is done again 256 columns at a time with
+// exact pruning. The merge does the same with the lists' maxima: only lists
+// whose maximum reaches the k-th largest of them are read.
 //
-// Bound by HBM for large batches (one read of s bytes an element, one
-// exponential), by latency for a few rows.
+// Bound by latency for a few rows, by instruction issue for many (about ten
+// instructions an element, one exponential among them; HBM would allow
+// three).
 #include <climits>
 
 #include "kld_internal.h"
@@ -35,6 +38,7 @@ using packed::Type;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;                // of the selection
 constexpr int kPer = 16;                     // columns of a thread per tile
 constexpr int kList = 1024;                  // entries of the shared list
 constexpr float kL = 1.4426950408889634f;
@@ -56,47 +60,52 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ double warp_max(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
 __device__ __forceinline__ uint64_t order_key(double x) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+// The same of an fp32 value, in 32 bits.
+__device__ __forceinline__ uint32_t order_key32(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value32(uint32_t k) {
+  return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
 }
 __device__ __forceinline__ double key_value(uint64_t k) {
   const uint64_t b = (k >> 63) ? (k & 0x7fffffffffffffffull) : ~k;
   return __longlong_as_double(static_cast<long long>(b));
 }
 
-// The n-th largest (n >= 1) of the warp's values, ties counted apart; -inf
-// when fewer than n are above -inf.
-template <typename T>
-__device__ __forceinline__ T warp_nth(T x, int n) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const T none = -INFINITY;
-  T m = warp_max(x);
-  for (int i = 1; i < n; ++i) {
-    const unsigned who = __ballot_sync(0xffffffffu, x == m);
-    if (lane == __ffs(static_cast<int>(who)) - 1) x = none;
-    m = warp_max(x);
-  }
-  return m;
-}
-
 // A lower bound of the k-th largest value of the CTA from one value per
-// thread: the least of the warps' ceil(k / warps)-th largest.
-template <typename T>
-__device__ __forceinline__ T block_bound(T x, int k, T* sh) {
-  const T m = warp_nth(x, (k + kWarps - 1) / kWarps);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+// thread: the k-th largest of every warp's `each` (<= 32) largest, -inf when
+// those are fewer than k.
+struct BoundShared {
+  float cand[kWarps * 32];
+  float bound;
+};
+__device__ __forceinline__ float block_bound(float x, int k, int each, BoundShared& sh) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const float none = neg_inf();
+  for (int i = 0; i < each; ++i) {
+    const float m = warp_max(x);
+    const unsigned who = __ballot_sync(0xffffffffu, x == m);
+    if (lane == __ffs(static_cast<int>(who)) - 1) {
+      sh.cand[warp * each + i] = x;
+      x = none;
+    }
+  }
   __syncthreads();
-  T t = sh[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) t = sh[w] < t ? sh[w] : t;
+  const int n = kWarps * each;  // callers give each >= k / kWarps
+  if (tid < n) {
+    const float v = sh.cand[tid];
+    int above = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) above += sh.cand[i] > v || (sh.cand[i] == v && i < tid) ? 1 : 0;
+    if (above == k - 1) sh.bound = v;
+  }
   __syncthreads();
-  return t;
+  return sh.bound;
 }
 
 // The shared list: order keys of the values and their indices (a key's ties
@@ -133,9 +142,11 @@ __device__ void prune(List& l, int k) {
     if (e * kThreads >= n) break;
     if (static_cast<int>(threadIdx.x) + e * kThreads >= n) continue;
     int c = 0;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const uint64_t o = l.key[i];
-      c += (o > key[e] || (o == key[e] && l.idx[i] < idx[e])) ? 1 : 0;
+      const uint32_t j = l.idx[i];
+      c += static_cast<int>(o > key[e]) + static_cast<int>(o == key[e] && j < idx[e]);
     }
     rank[e] = c;
   }
@@ -163,8 +174,7 @@ struct Select {
   int64_t slice;            // columns per CTA (a multiple of the tile's)
   int cap;                  // entries a CTA may leave
   // workspace
-  float2* sums;             // [rows * parts]: frame m, sum of e^(x - m)
-  int* counts;              // [rows * parts]
+  float4* sums;             // [rows * parts]: frame m, sum of e^(x - m), largest entry, entries (bits)
   float2* entries;          // [rows * parts][cap]: value, column (bits)
   unsigned* tickets;        // [groups], zero between launches
   uint32_t* flags;
@@ -174,16 +184,21 @@ struct Select {
   int32_t* out_parents;
 };
 
+constexpr int kMaxLists = kBeamMaxLists;
+
 struct SelectShared {
   List list;
-  float bound[kWarps];
-  double dbound[kWarps];
+  BoundShared bound;
   float F[kWarps], S[kWarps];
-  int kept;
   int last;
+  // the merge
   float m[KLD_BEAM_MAX_BEAMS];      // lse = m + lns
   double lns[KLD_BEAM_MAX_BEAMS];   // NaN: the beam offers nothing
   float score[KLD_BEAM_MAX_BEAMS];
+  int chosen;
+  float top[kMaxLists];             // the lists' largest entries
+  uint16_t count[kMaxLists];
+  uint32_t choice[kMaxLists];       // beam << 16 | list
 };
 
 // Column j of a row, -inf outside.
@@ -201,6 +216,13 @@ struct Tile {
   uint32_t w[4 * NV];
   __device__ void load(const char* row, int64_t j0, int64_t j1, int64_t V, int off) {
     // columns [j0, j1) of the vector grid, which starts `off` columns before the row
+    constexpr int64_t kCols = static_cast<int64_t>(kThreads) * kPer;
+    if (j0 >= off && j0 + kCols <= j1 && j0 - off + kCols <= V) {  // the whole tile, for all threads
+      const uint4* p = reinterpret_cast<const uint4*>(row + (j0 - off) * Type<DT>::kBytes) + threadIdx.x;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(p + v * kThreads);
+      return;
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t g = j0 + (v * kThreads + static_cast<int>(threadIdx.x)) * E;
@@ -220,6 +242,70 @@ struct Tile {
   __device__ static int64_t column(int64_t j0, int k, int off) {
     return j0 + ((k / E) * kThreads + static_cast<int>(threadIdx.x)) * E + k % E - off;
   }
+  // The lane's maximum, and the sum of e^(lambda (x - F)) (16-bit values are
+  // never widened for either).
+  __device__ __forceinline__ float max() const {
+    if constexpr (DT == KLD_F32) {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int k = 1; k < 16; ++k) m = fmaxf(m, __uint_as_float(w[k]));
+      return m;
+    } else {
+      uint32_t m = w[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        if constexpr (DT == KLD_BF16)
+          asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[k]));
+        else
+          asm("max.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[k]));
+      }
+      return fmaxf(lo(m), hi(m));
+    }
+  }
+  __device__ __forceinline__ static float lo(uint32_t x) {
+    if constexpr (DT == KLD_BF16) return __uint_as_float(x << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(x & 0xffffu)));
+  }
+  __device__ __forceinline__ static float hi(uint32_t x) {
+    if constexpr (DT == KLD_BF16) return __uint_as_float(x & 0xffff0000u);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16)));
+  }
+  __device__ __forceinline__ float sum(float F) const {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float d0, d1;
+      if constexpr (DT == KLD_F32) {
+        d0 = __uint_as_float(w[2 * k]) - F;
+        d1 = __uint_as_float(w[2 * k + 1]) - F;
+      } else if constexpr (DT == KLD_BF16) {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tsub.f32.bf16 %0, lo, %3;\n\t"
+            "sub.f32.bf16 %1, hi, %3;\n\t}"
+            : "=f"(d0), "=f"(d1) : "r"(w[k]), "f"(F));
+      } else {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tsub.f32.f16 %0, lo, %3;\n\t"
+            "sub.f32.f16 %1, hi, %3;\n\t}"
+            : "=f"(d0), "=f"(d1) : "r"(w[k]), "f"(F));
+      }
+      s0 += ex2(d0 * kL);
+      s1 += ex2(d1 * kL);
+    }
+    return s0 + s1;
+  }
+  __device__ __forceinline__ float value(int k) const {
+    if constexpr (DT == KLD_F32) return __uint_as_float(w[k]);
+    else return (k & 1) ? hi(w[k >> 1]) : lo(w[k >> 1]);
+  }
+  // Bits of the elements that are >= T and above -inf.
+  __device__ __forceinline__ unsigned at_least(float T) const {
+    unsigned hits = 0u;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const float x = value(k);
+      hits |= x >= T && x > neg_inf() ? 1u << k : 0u;
+    }
+    return hits;
+  }
 };
 
 // Best k entries of columns [g0, g1) of the vector grid, exactly, 256 columns
@@ -235,7 +321,7 @@ __device__ __noinline__ void slow_part(List& l, const char* row, int64_t g0, int
   for (int64_t g = g0; g < g1; g += kThreads) {
     const int64_t j = g + threadIdx.x - off;
     const float x = g + threadIdx.x < g1 ? value_at<DT>(row, j, V) : neg_inf();
-    const uint64_t key = order_key(static_cast<double>(x));
+    const uint64_t key = order_key32(x);
     // columns rise, so an equal value later never replaces an earlier one
     if (x > neg_inf() && (!full || key > least)) push(l, key, static_cast<uint32_t>(j));
     __syncthreads();
@@ -250,7 +336,7 @@ __device__ __noinline__ void slow_part(List& l, const char* row, int64_t g0, int
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Select a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(const Select a) {
   __shared__ SelectShared sh;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int64_t part = blockIdx.x;
@@ -262,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
   const bool live = !done && score > neg_inf() && score < INFINITY;
   if (tid == 0) {
     sh.list.count = 0;
-    sh.kept = 0;
     if (!(score < INFINITY) && part % a.parts == 0) atomicOr(a.flags, KLD_BEAM_BAD_SCORE);
   }
   __syncthreads();
@@ -274,31 +359,34 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
     int64_t g1 = g0 + a.slice;
     if (g1 > V + off) g1 = V + off;
     constexpr int64_t kTile = static_cast<int64_t>(kThreads) * kPer;
-    float F = kLowest, S = 0.f, T = neg_inf();
-    Tile<DT> t;
-    if (g0 < g1) t.load(row, g0, g1, V, off);
+    float F = kLowest, S = 0.f, T = neg_inf(), top = neg_inf();  // top: of the lane, so far
+    int renew = 0, tile = 0;  // the tile that renews the bound next
+    Tile<DT> next;
+    if (g0 < g1) next.load(row, g0, g1, V, off);
     for (int64_t g = g0; g < g1; g += kTile) {
-      float x[kPer];
-      Type<DT>::unpack16(t.w, x);
-      if (g + kTile < g1) t.load(row, g + kTile, g1, V, off);
-      float m = x[0];
-#pragma unroll
-      for (int k = 1; k < kPer; ++k) m = fmaxf(m, x[k]);
+      const Tile<DT> t = next;
+      if (g + kTile < g1) next.load(row, g + kTile, g1, V, off);
+      const float m = fmaxf(t.max(), neg_inf());  // -inf where all are NaN
       if (m > F + kRaise) {
         S *= ex2((F - m) * kL);
         F = m;
       }
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) s += ex2((x[k] - F) * kL);
-      S += s;
-      if (g == g0) T = block_bound(m, a.k, sh.bound);
+      S += t.sum(F);
+      top = fmaxf(top, m);
+      if (tile++ == renew) {
+        // after 1, 2, 4, 8, ... tiles: each time about k more entries pass
+        T = block_bound(top, a.k, min(32, a.k / kWarps + 5), sh.bound);
+        renew = 2 * renew + 1;
+      }
       if (m >= T && m > neg_inf()) {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (x[k] >= T && x[k] > neg_inf())
-            push(sh.list, order_key(static_cast<double>(x[k])),
-                 static_cast<uint32_t>(Tile<DT>::column(g, k, off)));
+        // Only the columns are noted: taking a value out of 16 registers by
+        // its number costs more than reading the few again at the end.
+        for (unsigned hits = t.at_least(T); hits; hits &= hits - 1u) {
+          const int at = atomicAdd(&sh.list.count, 1);
+          if (at < kList)
+            sh.list.idx[at] =
+                static_cast<uint32_t>(Tile<DT>::column(g, __ffs(static_cast<int>(hits)) - 1, off));
+        }
       }
     }
     // this CTA's frame and sum
@@ -313,43 +401,39 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
       }
     }
     __syncthreads();
-    int n = sh.list.count;
-    if (n > kList) {
+    if (sh.list.count > kList) {
       slow_part<DT>(sh.list, row, g0, g1, off, V, a.k);
-      n = sh.list.count;
-    }
-    double T2 = -INFINITY;
-    if (n > a.cap) {
-      double best = -INFINITY;
-      for (int i = tid; i < n; i += kThreads) best = fmax(best, key_value(sh.list.key[i]));
-      T2 = block_bound(best, a.k, sh.dbound);
-    }
-    float2* to = a.entries + part * a.cap;
-    for (int i = tid; i < n; i += kThreads) {
-      const double x = key_value(sh.list.key[i]);
-      if (x >= T2) {
-        const int at = atomicAdd(&sh.kept, 1);
-        if (at < a.cap) to[at] = make_float2(static_cast<float>(x), __uint_as_float(sh.list.idx[i]));
-      }
-    }
-    __syncthreads();
-    if (sh.kept > a.cap) {  // ties at the bound: the exact k best
-      prune(sh.list, a.k);
-      if (tid < sh.list.count)
-        to[tid] = make_float2(static_cast<float>(key_value(sh.list.key[tid])),
-                              __uint_as_float(sh.list.idx[tid]));
-      if (tid == 0) sh.kept = sh.list.count;
+    } else {
+      for (int i = tid; i < sh.list.count; i += kThreads)
+        sh.list.key[i] = order_key32(value_at<DT>(row, sh.list.idx[i], V));
       __syncthreads();
+      if (sh.list.count > a.cap) prune(sh.list, a.k);
     }
+    const int n = sh.list.count;
+    float2* to = a.entries + part * a.cap;
+    top = neg_inf();
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = key_value32(static_cast<uint32_t>(sh.list.key[i]));
+      top = fmaxf(top, x);
+      to[i] = make_float2(x, __uint_as_float(sh.list.idx[i]));
+    }
+    top = warp_max(top);
+    __syncthreads();
+    if (lane == 0) sh.bound.cand[warp] = top;
+    __syncthreads();
     if (tid == 0) {
       float f = sh.F[0];
-      for (int w = 1; w < kWarps; ++w) f = fmaxf(f, sh.F[w]);
+      for (int w = 1; w < kWarps; ++w) {
+        f = fmaxf(f, sh.F[w]);
+        top = fmaxf(top, sh.bound.cand[w]);
+      }
       double s = 0.0;
       for (int w = 0; w < kWarps; ++w) s += scale_of(sh.F[w], f) * sh.S[w];
-      a.sums[part] = make_float2(f, static_cast<float>(s));
+      a.sums[part] = make_float4(f, static_cast<float>(s), top, __int_as_float(n));
     }
+  } else if (tid == 0) {
+    a.sums[part] = make_float4(kLowest, 0.f, neg_inf(), __int_as_float(0));
   }
-  if (tid == 0) a.counts[part] = live ? sh.kept : 0;
 
   // ---- the group's last CTA merges
   __threadfence();
@@ -376,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
       f = warp_max(f);
       double s = 0.0;
       for (int p = lane; p < a.parts; p += 32) {
-        const float2 v = __ldcg(a.sums + part0 + static_cast<int64_t>(w) * a.parts + p);
+        const float4 v = __ldcg(a.sums + part0 + static_cast<int64_t>(w) * a.parts + p);
         s += scale_of(v.x, f) * v.y;
       }
 #pragma unroll
@@ -393,38 +477,93 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
       sh.score[w] = sc;
     }
   }
-  if (tid == 0) sh.list.count = 0;
+  if (tid == 0) sh.list.count = sh.chosen = 0;
+  const int lists = a.beams * a.parts;
+  for (int l = tid; l < lists; l += kThreads) {
+    const float4 v = __ldcg(a.sums + part0 + l);
+    sh.top[l] = v.z;
+    sh.count[l] = static_cast<uint16_t>(__float_as_int(v.w));
+  }
   __syncthreads();
 
-  const int lists = a.beams * a.parts;
-  // Score of entry i of list l; false when there is none.
-  auto scored = [&](int l, int i, double& s, uint32_t& flat) {
-    const int w = l / a.parts;
-    const double lns = sh.lns[w];
-    if (!(lns == lns)) return false;
-    const float2 e = __ldcg(a.entries + (part0 + l) * a.cap + i);
-    s = static_cast<double>(sh.score[w]) +
-        ((static_cast<double>(e.x) - static_cast<double>(sh.m[w])) - lns);
-    flat = static_cast<uint32_t>(w) * static_cast<uint32_t>(V) + __float_as_uint(e.y);
-    return true;
+  // The score of a value of beam w (NaN: the beam offers nothing).
+  auto scored = [&](int w, float x) {
+    return static_cast<double>(sh.score[w]) +
+           ((static_cast<double>(x) - static_cast<double>(sh.m[w])) - sh.lns[w]);
   };
-  double best = -INFINITY;
-  for (int l = warp; l < lists; l += kWarps) {
-    const int n = __ldcg(a.counts + part0 + l);
-    for (int i = lane; i < n; i += 32) {
-      double s;
-      uint32_t flat;
-      if (scored(l, i, s, flat)) best = fmax(best, s);
-    }
+  // Bounds are taken in fp32, scores rounded down: one instruction a maximum.
+  float best = neg_inf();
+  // list l goes to warp l % kWarps, so that few lists leave no warp without
+  for (int l = warp + kWarps * lane; l < lists; l += kThreads)
+    if (sh.count[l]) best = fmaxf(best, __double2float_rd(scored(l / a.parts, sh.top[l])));
+  float bound = block_bound(best, a.k, min(32, a.k / kWarps + 5), sh.bound);
+  for (int l = tid; l < lists; l += kThreads) {
+    const int w = l / a.parts;
+    if (sh.count[l] && scored(w, sh.top[l]) >= static_cast<double>(bound))
+      sh.choice[atomicAdd(&sh.chosen, 1)] = static_cast<uint32_t>(w) << 16 | static_cast<uint32_t>(l);
   }
-  const double bound = block_bound(best, a.k, sh.dbound);
-  for (int l = warp; l < lists; l += kWarps) {
-    const int n = __ldcg(a.counts + part0 + l);
-    for (int i = lane; i < n; i += 32) {
-      double s;
-      uint32_t flat;
-      if (scored(l, i, s, flat) && s >= bound) push(sh.list, order_key(s), flat);
+  __syncthreads();
+  // Entries of the chosen lists, `cap` (a power of two) places each.
+  const int shift = 31 - __clz(a.cap);
+  const int places = sh.chosen << shift;
+  constexpr int kHold = 8;  // places a thread reads at a time
+  float2 v[kHold];
+  auto read = [&](int e0) {  // places e0 + i * kThreads, all on their way together
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int e = e0 + i * kThreads;
+      const int l = e < places ? sh.choice[e >> shift] & 0xffffu : 0, at = e & (a.cap - 1);
+      const bool have = e < places && at < sh.count[l];
+      v[i] = have ? __ldcg(a.entries + (part0 + l) * a.cap + at) : make_float2(neg_inf(), 0.f);
     }
+  };
+  auto best_of = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (v[i].x > neg_inf())
+        best = fmaxf(best, __double2float_rd(scored(sh.choice[(e0 + i * kThreads) >> shift] >> 16, v[i].x)));
+  };
+  auto offer = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      if (v[i].x > neg_inf()) {
+        const uint32_t w = sh.choice[(e0 + i * kThreads) >> shift] >> 16;
+        const double s = scored(w, v[i].x);
+        if (s >= static_cast<double>(bound))
+          push(sh.list, order_key(s), w * static_cast<uint32_t>(V) + __float_as_uint(v[i].y));
+      }
+    }
+  };
+  constexpr int kStep = kThreads * kHold;
+  auto offer_all = [&]() {
+    if (places <= kStep) {
+      offer(tid);
+    } else {
+      for (int e = tid; e < places; e += kStep) {
+        read(e);
+        offer(e);
+      }
+    }
+    __syncthreads();
+  };
+  if (places <= kStep) read(tid);
+  offer_all();
+  if (sh.list.count > kThreads) {
+    // Few lists for k, or long ones: a closer bound from their entries (a
+    // list holds at least k, or all its part has).
+    best = neg_inf();
+    if (places <= kStep) {
+      best_of(tid);
+    } else {
+      for (int e = tid; e < places; e += kStep) {
+        read(e);
+        best_of(e);
+      }
+    }
+    bound = fmaxf(bound, block_bound(best, a.k, min(32, max(a.k, 5)), sh.bound));
+    if (tid == 0) sh.list.count = 0;
+    __syncthreads();
+    offer_all();
   }
   auto offer_finished = [&]() {
     // a finished beam stays as it is: one candidate, its eos
@@ -438,17 +577,19 @@ __global__ void __launch_bounds__(kThreads, 4) kld_beam_select_kernel(const Sele
   offer_finished();
   __syncthreads();
   if (sh.list.count > kList) {
-    // ties at the bound: again, one list at a time with exact pruning
+    // ties at the bound: again, 256 places at a time with exact pruning
     __syncthreads();
     if (tid == 0) sh.list.count = 0;
     __syncthreads();
     offer_finished();
-    for (int l = 0; l < lists; ++l) {
-      const int n = __ldcg(a.counts + part0 + l);
-      for (int i = tid; i < n; i += kThreads) {
-        double s;
-        uint32_t flat;
-        if (scored(l, i, s, flat) && s >= bound) push(sh.list, order_key(s), flat);
+    for (int e = tid; e - tid < places; e += kThreads) {
+      const uint32_t c = e < places ? sh.choice[e >> shift] : 0u;
+      const int l = c & 0xffffu, at = e & (a.cap - 1);
+      if (e < places && at < sh.count[l]) {
+        const float2 x = __ldcg(a.entries + (part0 + l) * a.cap + at);
+        const double s = scored(c >> 16, x.x);
+        if (s >= static_cast<double>(bound))
+          push(sh.list, order_key(s), (c >> 16) * static_cast<uint32_t>(V) + __float_as_uint(x.y));
       }
       __syncthreads();
       if (sh.list.count > kList - kThreads) prune(sh.list, a.k);
@@ -601,16 +742,30 @@ cudaError_t launch_reorder_vec(const Reorder& a, unsigned grid, cudaStream_t s) 
 }  // namespace
 
 BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count) {
-  // About 16 slices an SM over all rows (four waves of four CTAs) keep the
-  // SMs evenly busy; a slice is at least one tile. parts * rows stays below
-  // 16 * SMs + 2 * rows, the workspace's size.
+  // CTAs per row: the number that takes the fewest rounds of CTAs times a
+  // CTA's time, in tiles, whose fixed part (the bound, the list, the ticket)
+  // is worth about kFixed of them. Measured at 256 rows of 151936 bf16: 8 parts
+  // 58 us, 2 parts (one round of 512) less; 8 rows take one tile a CTA.
+  // parts * rows stays below kBeamSlices + 2 * rows, the workspace's size.
   constexpr int64_t tile = static_cast<int64_t>(kThreads) * kPer;
-  BeamPlan p;
-  const int64_t target = static_cast<int64_t>(sm_count) * 16;
-  p.slice = (rows * V + target - 1) / target;
-  p.slice = (p.slice + tile - 1) / tile * tile;
+  constexpr int64_t kFixed = 4;
+  const int64_t slots = static_cast<int64_t>(sm_count) * kCtasPerSm;
   // the grid of vectors starts up to `off` columns before a row
-  p.parts = static_cast<int>((V + off + p.slice - 1) / p.slice);
+  const int64_t tiles = (V + off + tile - 1) / tile;
+  int64_t most = kBeamSlices / rows;
+  most = most < 1 ? 1 : (most < tiles ? most : tiles);
+  int64_t best = 1, cost = INT64_MAX;
+  for (int64_t n = 1; n <= most; ++n) {
+    const int64_t per = (tiles + n - 1) / n;
+    const int64_t c = (rows * n + slots - 1) / slots * (per + kFixed);
+    if (c < cost) {
+      cost = c;
+      best = per;
+    }
+  }
+  BeamPlan p;
+  p.slice = best * tile;
+  p.parts = static_cast<int>((tiles + best - 1) / best);
   return p;
 }
 
@@ -632,7 +787,6 @@ cudaError_t launch_beam_select(const BeamSelect& b, int sm_count, cudaStream_t s
   a.slice = p.slice;
   a.cap = b.cap;
   a.sums = b.sums;
-  a.counts = b.counts;
   a.entries = b.entries;
   a.tickets = b.tickets;
   a.flags = b.flags;

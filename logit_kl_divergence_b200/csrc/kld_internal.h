@@ -240,9 +240,12 @@ struct PackedRows {
 };
 cudaError_t launch_packed_rows(const PackedRows& a, int sm_count, cudaStream_t stream);
 
-// Beam selection (see kld_beam_select). Workspace: sums and counts of
-// `parts` entries, entries of parts * cap, parts <= 16 * SMs + 2 * rows;
-// tickets: one per group, zero between launches; flags: KLD_BEAM_* bits.
+// Beam selection (see kld_beam_select). Workspace: sums of `parts` entries,
+// entries of parts * cap (cap a power of two), parts <= kBeamSlices + 2 * rows
+// over all rows; tickets: one per group, zero between launches; flags:
+// KLD_BEAM_* bits.
+constexpr int kBeamSlices = 2400;
+constexpr int kBeamMaxLists = kBeamSlices + 2 * KLD_BEAM_MAX_BEAMS;  // of one group
 struct BeamPlan {
   int parts;      // CTAs per row
   int64_t slice;  // columns of each
@@ -257,8 +260,7 @@ struct BeamSelect {
   int32_t eos;
   int groups, beams, k, cap;
   int64_t V;
-  float2* sums;
-  int* counts;
+  float4* sums;
   float2* entries;
   unsigned* tickets;
   uint32_t* flags;

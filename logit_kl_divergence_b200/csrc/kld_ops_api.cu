@@ -17,8 +17,7 @@ struct kld_beam_s {
   int sm_count = 0;
   int max_groups = 0, max_beams = 0, max_k = 0, cap = 0;
   void* mem = nullptr;
-  float2* sums = nullptr;
-  int* counts = nullptr;
+  float4* sums = nullptr;
   float2* entries = nullptr;
   unsigned* tickets = nullptr;
   uint32_t* flags = nullptr;
@@ -100,16 +99,19 @@ kld_status_t kld_beam_create(kld_beam_t* out, int max_groups, int max_beams, int
   h->max_groups = max_groups;
   h->max_beams = max_beams;
   h->max_k = max_k;
-  h->cap = 2 * max_k < 64 ? 64 : 2 * max_k;
+  // Entries a CTA may leave (a power of two; it leaves about k for every
+  // doubling of its tiles); past this it leaves its exact k.
+  h->cap = 128;
+  while (h->cap < 8 * max_k) h->cap *= 2;
   // One allocation; plan_beam keeps parts * rows within this many parts.
   auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
-  const size_t parts = static_cast<size_t>(sms) * 16 +
+  const size_t parts = static_cast<size_t>(kld::kBeamSlices) +
                        2 * static_cast<size_t>(max_groups) * static_cast<size_t>(max_beams);
-  const size_t sums_b = up(parts * sizeof(float2)), counts_b = up(parts * sizeof(int));
+  const size_t sums_b = up(parts * sizeof(float4));
   const size_t entries_b = up(parts * static_cast<size_t>(h->cap) * sizeof(float2));
   const size_t tickets_b = up(static_cast<size_t>(max_groups) * sizeof(unsigned) + sizeof(uint32_t));
   kld_status_t st = KLD_OK;
-  cudaError_t err = cudaMalloc(&h->mem, tickets_b + sums_b + counts_b + entries_b);
+  cudaError_t err = cudaMalloc(&h->mem, tickets_b + sums_b + entries_b);
   if (err != cudaSuccess) {
     h->mem = nullptr;
     st = cuda_fail(err, "cudaMalloc(beam workspace)");
@@ -126,9 +128,8 @@ kld_status_t kld_beam_create(kld_beam_t* out, int max_groups, int max_beams, int
   char* m = static_cast<char*>(h->mem);
   h->tickets = reinterpret_cast<unsigned*>(m);
   h->flags = h->tickets + max_groups;
-  h->sums = reinterpret_cast<float2*>(m + tickets_b);
-  h->counts = reinterpret_cast<int*>(m + tickets_b + sums_b);
-  h->entries = reinterpret_cast<float2*>(m + tickets_b + sums_b + counts_b);
+  h->sums = reinterpret_cast<float4*>(m + tickets_b);
+  h->entries = reinterpret_cast<float2*>(m + tickets_b + sums_b);
   *out = h;
   return KLD_OK;
 }
@@ -175,7 +176,6 @@ kld_status_t kld_beam_select(kld_beam_t h, const void* logits, int64_t ld, kld_d
   b.cap = h->cap;
   b.V = V;
   b.sums = h->sums;
-  b.counts = h->counts;
   b.entries = h->entries;
   b.tickets = h->tickets;
   b.flags = h->flags;
