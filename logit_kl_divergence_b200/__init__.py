@@ -20,7 +20,7 @@ from ._lib import (BEAM_BAD_PARENT, BEAM_BAD_SCORE, BEAM_NONFINITE, KLD_BF16,  #
                    KLD_F16, KLD_F32, ROW_BAD_TOKEN, ROW_EMPTY, ROW_INF_KL, ROW_INF_NLL,
                    ROW_INF_NLL_BASE, ROW_NONFINITE, KLDError)
 from .beam import BeamSearch, BeamStates
-from .packed import PACK_BLOCK, PackedLogits, _on, pack_logits
+from .packed import PACK_BLOCK, PackedLogits, _empty, _on, pack_logits
 
 __all__ = ["KLDStats", "kld_stats", "run_static", "result_from_bytes", "plan", "dtype_code",
            "ROW_RECORD_BYTES", "selftest_bounded_wait", "PackedLogits", "pack_logits", "PACK_BLOCK",
@@ -158,22 +158,22 @@ class KLDStats:
             dt = dtype_code(quant)
             if not quant.is_contiguous():
                 raise ValueError("quant must be contiguous")
-            dense = _ptr(quant)
+            dense = quant.data_ptr()
         if token_ids is not None:
             if token_ids.dtype != torch.int32 or token_ids.dim() != 1 or token_ids.shape[0] != n:
                 raise ValueError("token_ids must be an int32 [N] tensor")
             if not token_ids.is_contiguous() or token_ids.device != self.device:
                 raise ValueError("token_ids must be contiguous and on the handle's device")
-        s, ctx = _on(stream, self.device)
+        s = _on(stream, self.device)
         rows, fields = None, None
         if per_row:
-            with ctx:
-                f64 = torch.empty((2, n), dtype=torch.float64, device=self.device)
-                i32 = torch.empty((2, n), dtype=torch.int32, device=self.device)
-            rows = {"kld": f64[0], "nll": f64[1], "amax_b": i32[0], "amax_q": i32[1]}
-            fields = ctypes.byref(_lib.Fields(*(t.data_ptr() for t in rows.values())))
-        head = (self._h, ctypes.byref(base._c), dense, dt, packed, _ptr(token_ids), n, vocab)
-        return head, fields, rows, s, ctx
+            kld, nll = _empty(stream, (2, n), torch.float64, self.device).unbind(0)
+            amax_b, amax_q = _empty(stream, (2, n), torch.int32, self.device).unbind(0)
+            rows = {"kld": kld, "nll": nll, "amax_b": amax_b, "amax_q": amax_q}
+            fields = ctypes.byref(_lib.Fields(kld.data_ptr(), nll.data_ptr(), amax_b.data_ptr(),
+                                              amax_q.data_ptr()))
+        tok = None if token_ids is None else token_ids.data_ptr()
+        return (self._h, ctypes.byref(base._c), dense, dt, packed, tok, n, vocab), fields, rows, s
 
     def run_packed(self, base: PackedLogits, quant, token_ids: torch.Tensor | None = None,
                    per_row: bool = False, stream=None) -> dict | None:
@@ -183,9 +183,8 @@ class KLDStats:
         ``per_row``, returns ``kld`` and ``nll`` (float64), ``amax_b`` and
         ``amax_q`` (int32) as CUDA tensors of N values. Asynchronous on the
         stream."""
-        head, fields, rows, s, _ = self._packed_call(base, quant, token_ids, per_row, stream)
-        _lib.check(self._lib.kld_stats_run_packed(*head, fields, ctypes.c_void_p(s.cuda_stream)),
-                   "kld_stats_run_packed")
+        head, fields, rows, s = self._packed_call(base, quant, token_ids, per_row, stream)
+        _lib.check(self._lib.kld_stats_run_packed(*head, fields, s), "kld_stats_run_packed")
         return rows
 
     def run_grad_packed(self, base: PackedLogits, quant, token_ids: torch.Tensor | None = None,
@@ -196,16 +195,14 @@ class KLDStats:
         logits' by default, float32 for packed ones), from one read of the
         rows. Returns the gradient, or (gradient, rows) with ``per_row``.
         Asynchronous on the stream."""
-        head, fields, rows, s, ctx = self._packed_call(base, quant, token_ids, per_row, stream)
+        head, fields, rows, s = self._packed_call(base, quant, token_ids, per_row, stream)
         if out is None:
             dt = grad_dtype or (torch.float32 if isinstance(quant, PackedLogits) else quant.dtype)
-            with ctx:
-                out = torch.empty(base.shape, dtype=dt, device=self.device)
+            out = _empty(stream, base.shape, dt, self.device)
         if tuple(out.shape) != base.shape or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out must be a contiguous [N, V] tensor on the logits' device")
-        _lib.check(self._lib.kld_stats_run_grad_packed(*head, _ptr(out), dtype_code(out), float(scale), fields,
-                                                       ctypes.c_void_p(s.cuda_stream)),
-                   "kld_stats_run_grad_packed")
+        _lib.check(self._lib.kld_stats_run_grad_packed(*head, out.data_ptr(), dtype_code(out), float(scale),
+                                                       fields, s), "kld_stats_run_grad_packed")
         return (out, rows) if per_row else out
 
     def run_topk(self, base: torch.Tensor, quant: torch.Tensor, token_ids: torch.Tensor | None = None,

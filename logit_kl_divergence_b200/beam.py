@@ -15,11 +15,11 @@ import ctypes
 import torch
 
 from . import _lib
-from .packed import _DTYPES, _on
+from .packed import _DTYPES, _empty, _on
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _span(t: torch.Tensor) -> tuple[int, int]:
@@ -166,20 +166,21 @@ class BeamSearch:
                 raise ValueError("finished must be contiguous and on the handle's device")
             if eos is None:
                 raise ValueError("finished beams need eos")
-        s, ctx = _on(stream, self.device)
-        shape = (groups, int(k))
+        s = _on(stream, self.device)
+        k = int(k)
         if out is None:
-            with ctx:
-                both = torch.empty((2, *shape), dtype=torch.int32, device=self.device)
-                out = (torch.empty(shape, dtype=torch.float32, device=self.device), both[0], both[1])
-        for t, dt in zip(out, (torch.float32, torch.int32, torch.int32)):
-            if t.shape != shape or t.dtype != dt or t.device != self.device or not t.is_contiguous():
-                raise ValueError("out must be contiguous float32, int32 and int32 [groups, k] tensors")
+            # one allocation: scores, tokens, parents
+            top, tokens, parents = _empty(stream, (3, groups, k), torch.int32, self.device).unbind(0)
+            out = (top.view(torch.float32), tokens, parents)
+        else:
+            for t, dt in zip(out, (torch.float32, torch.int32, torch.int32)):
+                if t.shape != (groups, k) or t.dtype != dt or t.device != self.device or not t.is_contiguous():
+                    raise ValueError("out must be contiguous float32, int32 and int32 [groups, k] tensors")
         ld = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
-        _lib.check(self._lib.kld_beam_select(self._h, _ptr(logits), ld, _DTYPES[logits.dtype], _ptr(scores),
-                                             _ptr(finished), 0 if eos is None else int(eos), groups, beams,
-                                             logits.shape[1], int(k), _ptr(out[0]), _ptr(out[1]),
-                                             _ptr(out[2]), ctypes.c_void_p(s.cuda_stream)), "kld_beam_select")
+        _lib.check(self._lib.kld_beam_select(self._h, logits.data_ptr(), ld, _DTYPES[logits.dtype],
+                                             scores.data_ptr(), _ptr(finished), 0 if eos is None else int(eos),
+                                             groups, beams, logits.shape[1], k, out[0].data_ptr(),
+                                             out[1].data_ptr(), out[2].data_ptr(), s), "kld_beam_select")
         return out
 
     def bind(self, states) -> BeamStates:
@@ -216,10 +217,9 @@ class BeamSearch:
             a, b = _span(t)
             if any(a < y and x < b for x, y in states.spans):
                 raise ValueError("parents and lengths may not lie in a state")
-        s, _ = _on(stream, self.device)
-        _lib.check(self._lib.kld_beam_reorder(self._h, states._c, len(states), _ptr(parents), _ptr(lengths),
-                                              parents.shape[0], parents.shape[1],
-                                              ctypes.c_void_p(s.cuda_stream)), "kld_beam_reorder")
+        _lib.check(self._lib.kld_beam_reorder(self._h, states._c, len(states.tensors), parents.data_ptr(),
+                                              _ptr(lengths), parents.shape[0], parents.shape[1],
+                                              _on(stream, self.device)), "kld_beam_reorder")
 
     def status(self) -> int:
         """Wait for this handle's last call and return (and clear) the

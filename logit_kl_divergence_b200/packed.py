@@ -21,13 +21,22 @@ PACK_BLOCK = _lib.KLD_PACK_BLOCK
 _DTYPES = {torch.float32: _lib.KLD_F32, torch.bfloat16: _lib.KLD_BF16, torch.float16: _lib.KLD_F16}
 
 
-def _on(stream, device):
-    """(stream to launch on, context in which its outputs are allocated)."""
+def _on(stream, device) -> int:
+    """The handle of the stream to launch on."""
     if stream is None:
-        return torch.cuda.current_stream(device), torch.cuda.device(device)
+        return torch.cuda.current_stream(device).cuda_stream
     if stream.device != device:
         raise ValueError("the stream must be on the tensors' device")
-    return stream, torch.cuda.stream(stream)
+    return stream.cuda_stream
+
+
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """An output for a call on ``stream`` (None: the current one), allocated
+    in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class PackedLogits:
@@ -54,6 +63,8 @@ class PackedLogits:
         if codes.data_ptr() % 16:
             raise ValueError("codes must be aligned to 16 bytes")
         self.codes, self.heads, self.vocab = codes, heads, vocab
+        self.shape = (codes.shape[0], vocab)
+        self.device = codes.device
         self._c = _lib.Packed(codes.data_ptr(), heads.data_ptr())
 
     @classmethod
@@ -63,14 +74,6 @@ class PackedLogits:
         device = torch.device("cuda") if device is None else device
         return cls(torch.empty((n_rows, blocks * PACK_BLOCK), dtype=torch.uint8, device=device),
                    torch.empty((n_rows, blocks), dtype=torch.int32, device=device), vocab)
-
-    @property
-    def shape(self) -> tuple[int, int]:
-        return self.codes.shape[0], self.vocab
-
-    @property
-    def device(self) -> torch.device:
-        return self.codes.device
 
     @property
     def nbytes(self) -> int:
@@ -96,18 +99,16 @@ class PackedLogits:
         lib = _lib.load()
         if not self.codes.is_cuda:
             raise ValueError("the checkpoint must be on a CUDA device")
-        s, ctx = _on(stream, self.device)
+        s = _on(stream, self.device)
         if out is None:
-            with ctx:
-                out = torch.empty(self.shape, dtype=dtype, device=self.device)
+            out = _empty(stream, self.shape, dtype, self.device)
         if out.dtype not in _DTYPES:
             raise TypeError(f"unsupported logit dtype {out.dtype}")
         if out.shape != self.shape or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out must be a contiguous [N, vocab] tensor on the checkpoint's device")
         if len(self):
             _lib.check(lib.kld_unpack_logits(ctypes.byref(self._c), len(self), self.vocab,
-                                             ctypes.c_void_p(out.data_ptr()), _DTYPES[out.dtype],
-                                             self.device.index, ctypes.c_void_p(s.cuda_stream)),
+                                             out.data_ptr(), _DTYPES[out.dtype], self.device.index, s),
                        "kld_unpack_logits")
         return out
 
@@ -123,15 +124,15 @@ def pack_logits(logits: torch.Tensor, out: PackedLogits | None = None, stream=No
         raise ValueError("logits must be a [N, V] tensor")
     if not logits.is_cuda or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous CUDA tensor")
-    s, ctx = _on(stream, logits.device)
+    s = _on(stream, logits.device)
     if out is None:
-        with ctx:
-            out = PackedLogits.empty(logits.shape[0], logits.shape[1], logits.device)
+        n, blocks = logits.shape[0], -(-logits.shape[1] // PACK_BLOCK)
+        out = PackedLogits(_empty(stream, (n, blocks * PACK_BLOCK), torch.uint8, logits.device),
+                           _empty(stream, (n, blocks), torch.int32, logits.device), logits.shape[1])
     if out.shape != tuple(logits.shape) or out.device != logits.device:
         raise ValueError("out must hold as many rows and columns on the logits' device")
     if len(out):
-        _lib.check(lib.kld_pack_logits(ctypes.c_void_p(logits.data_ptr()), logits.shape[0],
-                                       logits.shape[1], _DTYPES[logits.dtype], ctypes.byref(out._c),
-                                       logits.device.index, ctypes.c_void_p(s.cuda_stream)),
+        _lib.check(lib.kld_pack_logits(logits.data_ptr(), logits.shape[0], logits.shape[1],
+                                       _DTYPES[logits.dtype], ctypes.byref(out._c), logits.device.index, s),
                    "kld_pack_logits")
     return out
