@@ -477,8 +477,9 @@ typedef struct kld_beam_s* kld_beam_t;
 /*
  * A handle for up to max_groups groups (prompts) of max_beams beams, keeping
  * up to max_k candidates a group (1 <= max_beams <= 64, 1 <= max_k <= 128).
- * Owns a device workspace (about 30 KB + 1 KB per row and candidate set),
- * released by kld_beam_destroy. Bound to one device, not thread-safe; calls
+ * Owns a device workspace of about (2400 + 2 rows) * (16 + 8 c) bytes, rows =
+ * max_groups * max_beams and c the power of two from max(128, 8 * max_k) on
+ * (2.6 MB for a few rows and max_k <= 16), released by kld_beam_destroy. Bound to one device, not thread-safe; calls
  * whose GPU work overlaps (other streams, graphs replayed at the same time)
  * need handles of their own.
  */

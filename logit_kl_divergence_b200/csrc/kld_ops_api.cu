@@ -41,6 +41,13 @@ kld_status_t check_matrix(const void* x, int64_t N, int64_t V, kld_dtype_t dtype
   return KLD_OK;
 }
 
+// Zeroes device memory before it returns: cudaMemset alone may still be under
+// way, and streams that do not wait for the default one would not wait for it.
+cudaError_t clear(void* p, size_t bytes) {
+  const cudaError_t e = cudaMemset(p, 0, bytes);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(nullptr);
+}
+
 // The event that kld_beam_status and kld_beam_destroy wait for; not part of
 // a captured graph (whose replays the caller waits for).
 kld_status_t mark_done(kld_beam_s* h, cudaStream_t s) {
@@ -115,7 +122,7 @@ kld_status_t kld_beam_create(kld_beam_t* out, int max_groups, int max_beams, int
   if (err != cudaSuccess) {
     h->mem = nullptr;
     st = cuda_fail(err, "cudaMalloc(beam workspace)");
-  } else if ((err = cudaMemset(h->mem, 0, tickets_b)) != cudaSuccess) {
+  } else if ((err = clear(h->mem, tickets_b)) != cudaSuccess) {
     st = cuda_fail(err, "cudaMemset");
   } else if ((err = cudaEventCreateWithFlags(&h->done, cudaEventDisableTiming)) != cudaSuccess) {
     h->done = nullptr;
@@ -226,7 +233,7 @@ kld_status_t kld_beam_status(kld_beam_t h, uint32_t* flags) {
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   KLD_CUDA(cudaEventSynchronize(h->done));
   KLD_CUDA(cudaMemcpy(flags, h->flags, sizeof(uint32_t), cudaMemcpyDeviceToHost));
-  KLD_CUDA(cudaMemset(h->flags, 0, sizeof(uint32_t)));
+  KLD_CUDA(clear(h->flags, sizeof(uint32_t)));
   return KLD_OK;
 }
 

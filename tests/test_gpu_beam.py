@@ -310,3 +310,24 @@ def test_beams_decoded_then_scored_against_the_saved_logits():
         st.run_packed(store, quant - 0.5 * grad, nxt)
         second = st.result()
         assert first["n_valid"] == rows * steps and second["mean_kld"] < first["mean_kld"]
+
+
+def test_flags_and_tickets_are_cleared_before_the_next_call():
+    """A handle made, or its flags read, right before a call on a stream that
+    does not wait for the default one."""
+    x = _rows(8, 4099, 3)
+    x[2, 17] = math.nan
+    x, scores = x.to(DEV), _scores(2, 4, 3).to(DEV)
+    side = torch.cuda.Stream(DEV)
+    big = torch.empty(64 << 20, device=DEV)
+    torch.cuda.synchronize()
+    want = None
+    for _ in range(20):
+        big.fill_(1.0)  # the default stream is busy
+        with BeamSearch(2, 4, max_k=8, device=DEV) as beam:
+            for _ in range(3):
+                got = beam.select(x, scores, 8, stream=side)
+                assert beam.status() == BEAM_NONFINITE
+                got = [t.cpu() for t in got]
+                want = want or got
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
