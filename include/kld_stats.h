@@ -416,7 +416,8 @@ typedef struct {
  * to the element size) into out->codes / out->heads (caller-owned DEVICE
  * memory of the sizes above). `device` is the device that holds them.
  * Asynchronous on `stream`; allocates nothing. KLD_ERR_INVALID_ARG for NULL
- * or misaligned pointers or sizes out of range, KLD_ERR_DTYPE.
+ * or misaligned pointers, memory that overlaps or sizes out of range,
+ * KLD_ERR_DTYPE.
  */
 kld_status_t kld_pack_logits(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
                              const kld_packed_t* out, int device, void* stream);
@@ -457,7 +458,9 @@ kld_status_t kld_stats_run_packed(kld_stats_t h, const kld_packed_t* base, const
  *   grad[i][j] = scale * (softmax(q_i)_j - softmax(b_i)_j)
  * of the restored values, zero on excluded rows, in one kernel that reads
  * the rows once. grad: caller-owned DEVICE memory, [N, V] of grad_dtype,
- * aligned to its element size. A non-finite scale is KLD_ERR_INVALID_ARG.
+ * aligned to its element size; it may be the dense quant rows themselves when
+ * grad_dtype is quant_dtype, and may not overlap the inputs otherwise. A
+ * non-finite scale is KLD_ERR_INVALID_ARG.
  */
 kld_status_t kld_stats_run_grad_packed(kld_stats_t h, const kld_packed_t* base, const void* quant,
                                        kld_dtype_t quant_dtype, const kld_packed_t* quant_packed,

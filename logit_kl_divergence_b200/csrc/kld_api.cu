@@ -169,7 +169,9 @@ kld_status_t run_packed(kld_stats_t h, const kld_packed_t* base, const void* qua
                         const int32_t* tok, int64_t N, int64_t V, void* grad,
                         kld_dtype_t grad_dtype, float scale, const kld_fields_t* fields,
                         void* stream) {
-  if (!h || !base || N < 1 || V < 1 || V > INT32_MAX || N > h->max_rows) return KLD_ERR_INVALID_ARG;
+  if (!h || !base || N < 1 || V < 1 || V > INT32_MAX || N > h->max_rows ||
+      N > INT64_MAX / 4 / (V + KLD_PACK_BLOCK))
+    return KLD_ERR_INVALID_ARG;
   auto bad = [](const kld_packed_t* p) {
     return !p->codes || !p->heads || (reinterpret_cast<uintptr_t>(p->codes) & 15u) ||
            (reinterpret_cast<uintptr_t>(p->heads) & 3u);
@@ -187,6 +189,26 @@ kld_status_t run_packed(kld_stats_t h, const kld_packed_t* base, const void* qua
     return KLD_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(f.amax_b) | reinterpret_cast<uintptr_t>(f.amax_q)) & 3u)
     return KLD_ERR_INVALID_ARG;
+  // What is written may not be read by the same call, but for the gradient
+  // over the very quant rows it belongs to.
+  const int64_t nb = (V + KLD_PACK_BLOCK - 1) / KLD_PACK_BLOCK;
+  const int64_t quant_bytes = quant_packed ? 0 : N * V * kld::elem_bytes(quant_dtype);
+  auto written = [&](const void* p, int64_t bytes, bool over_quant) {
+    auto clear_of = [&](const kld_packed_t* k) {
+      return !k || (kld::apart(p, bytes, k->codes, N * nb * KLD_PACK_BLOCK) &&
+                    kld::apart(p, bytes, k->heads, 4 * N * nb));
+    };
+    return clear_of(base) && clear_of(quant_packed) && kld::apart(p, bytes, tok, 4 * N) &&
+           (over_quant || kld::apart(p, bytes, quant, quant_bytes));
+  };
+  const int64_t grad_bytes = grad ? N * V * kld::elem_bytes(grad_dtype) : 0;
+  if (!written(grad, grad_bytes, grad == quant && grad_dtype == quant_dtype)) return KLD_ERR_INVALID_ARG;
+  const void* out[4] = {f.kld, f.nll, f.amax_b, f.amax_q};
+  for (int i = 0; i < 4; ++i) {
+    if (!written(out[i], (i < 2 ? 8 : 4) * N, false) ||
+        !kld::apart(out[i], (i < 2 ? 8 : 4) * N, grad, grad_bytes))
+      return KLD_ERR_INVALID_ARG;
+  }
   DeviceGuard guard(h->device);
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   cudaStream_t s = static_cast<cudaStream_t>(stream);

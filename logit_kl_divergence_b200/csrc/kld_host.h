@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 #include "kld_stats.h"
 
 namespace kld {
@@ -16,6 +18,13 @@ kld_status_t cuda_fail(cudaError_t e, const char* what);
     cudaError_t _e = (call);                                 \
     if (_e != cudaSuccess) return kld::cuda_fail(_e, #call); \
   } while (0)
+
+// Whether two ranges of bytes have none in common (a null or empty one has no bytes).
+inline bool apart(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return !a || !b || a_bytes <= 0 || b_bytes <= 0 || x + static_cast<uintptr_t>(a_bytes) <= y ||
+         y + static_cast<uintptr_t>(b_bytes) <= x;
+}
 
 // KLD_OK when `device` exists and is of compute capability 10.0; *sms: its
 // SM count.

@@ -38,6 +38,11 @@ kld_status_t check_matrix(const void* x, int64_t N, int64_t V, kld_dtype_t dtype
   if (!aligned(x, static_cast<uintptr_t>(kld::elem_bytes(dtype))) || !aligned(packed->codes, 16) ||
       !aligned(packed->heads, 4))
     return KLD_ERR_INVALID_ARG;
+  const int64_t nb = (V + KLD_PACK_BLOCK - 1) / KLD_PACK_BLOCK, bytes = N * V * kld::elem_bytes(dtype);
+  if (!kld::apart(x, bytes, packed->codes, N * nb * KLD_PACK_BLOCK) ||
+      !kld::apart(x, bytes, packed->heads, 4 * N * nb) ||
+      !kld::apart(packed->codes, N * nb * KLD_PACK_BLOCK, packed->heads, 4 * N * nb))
+    return KLD_ERR_INVALID_ARG;
   return KLD_OK;
 }
 
@@ -168,6 +173,15 @@ kld_status_t kld_beam_select(kld_beam_t h, const void* logits, int64_t ld, kld_d
   if (!aligned(logits, static_cast<uintptr_t>(kld::elem_bytes(dtype))) || !aligned(scores, 4) ||
       !aligned(scores_out, 4) || !aligned(tokens_out, 4) || !aligned(parents_out, 4))
     return KLD_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(groups) * beams, places = 4 * static_cast<int64_t>(groups) * k;
+  const int64_t read = ((rows - 1) * ld + V) * kld::elem_bytes(dtype);
+  const void* outs[3] = {scores_out, tokens_out, parents_out};
+  for (int i = 0; i < 3; ++i) {
+    if (!kld::apart(outs[i], places, logits, read) || !kld::apart(outs[i], places, scores, 4 * rows) ||
+        !kld::apart(outs[i], places, finished, rows) ||
+        !kld::apart(outs[i], places, outs[(i + 1) % 3], places))
+      return KLD_ERR_INVALID_ARG;
+  }
   DeviceGuard guard(h->device);
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   kld::BeamSelect b;

@@ -1,5 +1,5 @@
-// kld_packed_rows.cu -- the statistic and the gradient with packed base rows for
-// few rows (mathematics: kld_packed_rows.cuh).
+// kld_packed_rows.cu -- the statistic and the gradient with packed base rows
+// (mathematics: kld_packed_rows.cuh).
 //
 // One read of the logits for both passes. A row belongs to one CTA of four
 // warps, or, when there are few rows, to a cluster of 2, 4 or 8 of them, each
@@ -230,9 +230,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         x[k] = j < 0 || j >= V ? neg_inf() : (which ? quant_at<QT>(rp, j) : base_at<QT>(rp, j));
       }
       int at = INT_MAX;
+      const int64_t j0 = static_cast<int64_t>(c) * kChunk - off;
 #pragma unroll
-      for (int k = 15; k >= 0; --k)
-        if (x[k] == m) at = c * kChunk + group_col<QT>(k / Quant<QT>::kGroup, lane) + k % Quant<QT>::kGroup - off;
+      for (int k = 15; k >= 0; --k) {
+        if (x[k] == m)
+          at = static_cast<int>(j0 + group_col<QT>(k / Quant<QT>::kGroup, lane) + k % Quant<QT>::kGroup);
+      }
       if (C > 1)
         min_peer(smem_u32(which ? &sh.iq : &sh.ib), 0u, static_cast<uint32_t>(at));
       else
@@ -244,6 +247,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     Slow s;
     slow_row<QT>(sh.slow, rp, V, s);
     if (grow) {
+      if (C > 1) {  // the gradient may go over the quant rows: all have read them
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+      }
       const int64_t j0 = static_cast<int64_t>(c0) * kChunk - off;
       const int64_t j1 = static_cast<int64_t>(c1) * kChunk - off;
       slow_grad<QT, OT>(rp, j0 < 0 ? 0 : j0, j1 < V ? j1 : V, s, grow, out.scale);

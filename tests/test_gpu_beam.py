@@ -15,7 +15,7 @@ import torch
 
 import packed_ref
 from logit_kl_divergence_b200 import (BEAM_BAD_PARENT, BEAM_BAD_SCORE, BEAM_NONFINITE, BeamSearch,
-                                      KLDStats, PackedLogits, pack_logits)
+                                      KLDError, KLDStats, PackedLogits, pack_logits)
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -331,3 +331,16 @@ def test_flags_and_tickets_are_cleared_before_the_next_call():
                 got = [t.cpu() for t in got]
                 want = want or got
                 assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_outputs_over_inputs_are_refused():
+    x, scores = _rows(4, 100, 1).to(DEV), _scores(2, 2, 1).to(DEV)
+    free = [torch.empty((2, 2), dtype=dt, device=DEV) for dt in (torch.float32, torch.int32, torch.int32)]
+    with BeamSearch(2, 2, max_k=4, device=DEV) as beam:
+        for out in ((scores, free[1], free[2]), (free[0], free[1], free[1]),
+                    (free[0], scores.view(torch.int32), free[2]), (x[3, 96:].view(2, 2), free[1], free[2])):
+            with pytest.raises(KLDError):
+                beam.select(x, scores, 2, out=out)
+        done = torch.zeros((2, 2), dtype=torch.bool, device=DEV)
+        assert beam.select(x, scores, 2, finished=done, eos=3, out=tuple(free))[0] is free[0]
+        assert beam.status() == 0

@@ -25,7 +25,7 @@ import torch
 
 import oracle
 import packed_ref
-from logit_kl_divergence_b200 import KLDStats, PackedLogits, pack_logits, rows_view, synth
+from logit_kl_divergence_b200 import KLDError, KLDStats, PackedLogits, pack_logits, rows_view, synth
 
 from gpu_helpers import assert_rows_match, assert_stats_match
 
@@ -329,3 +329,49 @@ def test_packed_rows_leave_the_dense_path_as_it_was():
 def test_sizes_of_zero_rows():
     p = pack_logits(torch.empty((0, 300), device=DEV))
     assert p.shape == (0, 300) and p.unpack().shape == (0, 300)
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16"])
+@pytest.mark.parametrize("n,v", [(3, 40000), (1, 5), (700, 1003)])
+def test_gradient_over_the_quant_rows_themselves(quant, n, v):
+    """In place: the same gradient, rows done in fp64 (masked base entries
+    with finite quant ones and the reverse, a NaN row) included."""
+    b, q, tok = _pair(n, v, n + v)
+    if n > 2:
+        b[0, 1::2] = -math.inf
+        q[1, ::3] = -math.inf
+        q[2, v // 2] = math.nan
+    q = q.to(DTYPES[quant]).to(DEV)
+    base, tok = pack_logits(b.to(DEV)), tok.to(DEV)
+    with KLDStats(n, device=DEV) as st:
+        want, rows = st.run_grad_packed(base, q, tok, scale=0.5, per_row=True)
+        over = q.clone()
+        got, again = st.run_grad_packed(base, over, tok, out=over, scale=0.5, per_row=True)
+        assert got.data_ptr() == over.data_ptr() and torch.equal(got, want)
+        for name in rows:
+            assert torch.equal(rows[name].nan_to_num(nan=-1.0), again[name].nan_to_num(nan=-1.0))
+
+
+def test_outputs_over_inputs_are_refused():
+    n, v = 4, 256
+    mem = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+
+    def at(byte, dtype, *shape):
+        size = torch.empty((), dtype=dtype).element_size() * math.prod(shape)
+        return mem[byte:byte + size].view(dtype).view(*shape)
+
+    base = PackedLogits(at(0, torch.uint8, n, v), at(1024, torch.int32, n, 2), v)
+    quant, tok = at(2048, torch.bfloat16, n, v), at(4096, torch.int32, n)
+    with KLDStats(n, device=DEV) as st:
+        for byte, dtype in ((2048, torch.float16), (2046, torch.bfloat16), (4094, torch.bfloat16),
+                            (0, torch.bfloat16), (1022, torch.bfloat16), (1054, torch.float16), (4108, torch.float32)):
+            with pytest.raises(KLDError):
+                st.run_grad_packed(base, quant, tok, out=at(byte // 4 * 4 if dtype == torch.float32 else byte,
+                                                            dtype, n, v))
+        with pytest.raises(KLDError):
+            st.run_grad_packed(base, base, out=at(1020, torch.float32, n, v))
+        for byte in (0, 4112):  # before and behind all of them
+            st.run_grad_packed(PackedLogits(at(8192, torch.uint8, n, v), at(9216, torch.int32, n, 2), v), quant,
+                               tok, out=at(byte, torch.bfloat16, n, v))
+        st.run_grad_packed(base, quant, tok, out=quant)
+        st.result()

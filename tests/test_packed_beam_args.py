@@ -33,6 +33,17 @@ def test_pack_and_unpack_refuse(lib):
         assert f(pk=_pk(heads=P + 2)) == INVALID
 
 
+def test_pack_and_unpack_refuse_memory_that_overlaps(lib):
+    # 4 rows of 8 columns: 512 bytes of codes, 16 of headers, 128 of logits
+    at = lambda k: ctypes.c_void_p(P + k)
+    for f in (lambda x, c, h: lib.kld_pack_logits(at(x), 4, 8, 0, _pk(P + c, P + h), 1 << 20, None),
+              lambda x, c, h: lib.kld_unpack_logits(_pk(P + c, P + h), 4, 8, at(x), 0, 1 << 20, None)):
+        assert f(0, 112, 4096) == INVALID and f(508, 0, 4096) == INVALID and f(0, 0, 4096) == INVALID
+        assert f(0, 1024, 124) == INVALID and f(0, 1024, 1532) == INVALID and f(1552, 1024, 1540) == INVALID
+        if not torch.cuda.is_available():  # apart: only the device is missing
+            assert f(0, 128, 640) == _lib.KLD_ERR_NO_DEVICE and f(528, 0, 512) == _lib.KLD_ERR_NO_DEVICE
+
+
 def test_packed_runs_and_beams_refuse_a_null_handle(lib):
     x = ctypes.c_void_p(P)
     assert lib.kld_stats_run_packed(None, _pk(), x, 0, None, None, 1, 1, None, None) == INVALID
