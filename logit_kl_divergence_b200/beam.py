@@ -11,6 +11,7 @@ kernels (``include/kld_stats.h``: kld_beam_select, kld_beam_reorder).
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -28,6 +29,31 @@ def _span(t: torch.Tensor) -> tuple[int, int]:
         return t.data_ptr(), t.data_ptr()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(a: tuple, b: tuple) -> bool:
+    """Whether two states (span, layout, row count) share no byte. Layouts
+    that interleave are told apart by the strides they have in common; states
+    that this cannot show to be apart count as overlapping."""
+    (x0, x1), s, rows = a
+    (y0, y1), t, _ = b
+    if x1 <= y0 or y1 <= x0:
+        return True
+    run_s, run_t = s.positions * s.position_bytes, t.positions * t.position_bytes
+
+    def between(period, len_s, len_t):
+        gap = (y0 - x0) % period  # from s on to the next t, and from there to the next s
+        return gap >= len_s and period - gap >= len_t
+
+    if rows > 1 and s.row_stride == t.row_stride:
+        len_s = (s.outer - 1) * s.outer_stride + run_s
+        len_t = (t.outer - 1) * t.outer_stride + run_t
+        if between(s.row_stride, len_s, len_t):
+            return True
+    # all runs of both start whole multiples of their strides' common divisor apart
+    steps = [u.row_stride for u in (s, t) if rows > 1] + [u.outer_stride for u in (s, t) if u.outer > 1]
+    period = math.gcd(*steps)
+    return period > 0 and between(period, run_s, run_t)
 
 
 def _describe(t: torch.Tensor, time_dim: int | None) -> _lib.State:
@@ -89,11 +115,17 @@ class BeamStates:
         self.rows = rows.pop() if rows else None
         if any(t.device != device for t in self.tensors):
             raise ValueError("states must be on the handle's device")
-        starts = [t.data_ptr() for t in self.tensors if t.numel()]
-        if len(set(starts)) != len(starts):
-            raise ValueError("a state is given twice")
         self.spans = [_span(t) for t in self.tensors]
-        self._c = (_lib.State * max(1, len(items)))(*[_describe(t, d) for t, d in items])
+        layouts = [_describe(t, d) for t, d in items]
+        order = sorted(((span, layout, self.rows) for span, layout in zip(self.spans, layouts)
+                        if span[0] < span[1]), key=lambda a: a[0])
+        for i, a in enumerate(order):
+            for b in order[i + 1:]:
+                if b[0][0] >= a[0][1]:
+                    break
+                if not _apart(a, b):
+                    raise ValueError("states may not overlap one another")
+        self._c = (_lib.State * max(1, len(items)))(*layouts)
 
     def __len__(self) -> int:
         return len(self.tensors)

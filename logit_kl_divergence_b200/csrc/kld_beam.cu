@@ -625,6 +625,7 @@ struct StateDesc {
   int64_t row_stride, outer_stride;  // bytes
   int64_t run;                       // bytes of a full run (all positions)
   int64_t unit;                      // bytes of one position; 0: no time axis
+  int64_t positions;
   int32_t outer;
   uint32_t spans;                    // CTAs per run
   uint32_t first;                    // first CTA of this state
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(kThreads) kld_beam_reorder_kernel(const __grid
       n = s.run;
       if (a.lengths && s.unit) {
         const int64_t len = __ldg(a.lengths + group * a.beams + p);
-        n = len <= 0 ? 0 : (len * s.unit < n ? len * s.unit : n);
+        n = len <= 0 ? 0 : (len < s.positions ? len * s.unit : n);
       }
       if (n > x0) atomicMax(reinterpret_cast<unsigned long long*>(&longest),
                             static_cast<unsigned long long>(n));
@@ -806,6 +807,24 @@ cudaError_t launch_beam_select(const BeamSelect& b, int sm_count, cudaStream_t s
 cudaError_t launch_beam_reorder(const kld_state_t* states, int n, const int32_t* parents,
                                 const int32_t* lengths, int groups, int beams, uint32_t* flags,
                                 cudaStream_t stream) {
+  // A state's widest vectors, and its CTAs of them.
+  auto width_of = [&](const kld_state_t& t) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(t.data) | static_cast<uint64_t>(t.row_stride) |
+                          (t.outer > 1 ? static_cast<uint64_t>(t.outer_stride) : 0u);
+    int w = widest(beams);
+    while (w > 1 && (bits & static_cast<uint64_t>(w - 1))) w >>= 1;
+    return w;
+  };
+  auto spans_of = [&](const kld_state_t& t, int width) {
+    const int64_t span = static_cast<int64_t>(kThreads) * kSpan * width;
+    return (t.positions * t.position_bytes - 1) / span + 1;
+  };
+  constexpr int64_t kMostCtas = 0x7fffffff;
+  for (int i = 0; i < n; ++i) {  // refused before any is moved
+    const kld_state_t& t = states[i];
+    if (t.positions * t.position_bytes == 0 || t.outer == 0) continue;
+    if (spans_of(t, width_of(t)) > kMostCtas / t.outer / groups) return cudaErrorInvalidConfiguration;
+  }
   // One launch per vector width (and per kStatesPerLaunch states).
   for (int width = 16; width >= 1; width >>= 1) {
     Reorder a;
@@ -814,7 +833,7 @@ cudaError_t launch_beam_reorder(const kld_state_t* states, int n, const int32_t*
     a.parents = parents;
     a.lengths = lengths;
     a.flags = flags;
-    uint64_t grid = 0;
+    int64_t grid = 0;
     auto flush = [&]() -> cudaError_t {
       if (a.n == 0) return cudaSuccess;
       cudaError_t e;
@@ -834,24 +853,18 @@ cudaError_t launch_beam_reorder(const kld_state_t* states, int n, const int32_t*
       const kld_state_t& t = states[i];
       const int64_t run = t.positions * t.position_bytes;
       if (run == 0 || t.outer == 0) continue;
-      const uint64_t bits = reinterpret_cast<uintptr_t>(t.data) | static_cast<uint64_t>(t.row_stride) |
-                            (t.outer > 1 ? static_cast<uint64_t>(t.outer_stride) : 0u);
-      int w = widest(beams);
-      while (w > 1 && (bits & static_cast<uint64_t>(w - 1))) w >>= 1;
-      if (w != width) continue;
+      if (width_of(t) != width) continue;
       StateDesc d;
       d.p = static_cast<char*>(t.data);
       d.row_stride = t.row_stride;
       d.outer_stride = t.outer_stride;
       d.run = run;
       d.unit = t.timed ? t.position_bytes : 0;
+      d.positions = t.positions;
       d.outer = static_cast<int32_t>(t.outer);
-      const int64_t span = static_cast<int64_t>(kThreads) * kSpan * width;
-      d.spans = static_cast<uint32_t>((run + span - 1) / span);
-      const uint64_t ctas = static_cast<uint64_t>(d.spans) * static_cast<uint64_t>(t.outer) *
-                            static_cast<uint64_t>(groups);
-      if (ctas > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-      if (a.n == kStatesPerLaunch || grid + ctas > 0x7fffffffu) {
+      d.spans = static_cast<uint32_t>(spans_of(t, width));
+      const int64_t ctas = static_cast<int64_t>(d.spans) * t.outer * groups;
+      if (a.n == kStatesPerLaunch || grid + ctas > kMostCtas) {
         const cudaError_t e = flush();
         if (e != cudaSuccess) return e;
       }

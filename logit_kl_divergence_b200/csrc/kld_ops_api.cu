@@ -237,7 +237,9 @@ kld_status_t kld_beam_reorder(kld_beam_t h, const kld_state_t* states, int n,
   DeviceGuard guard(h->device);
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  KLD_CUDA(kld::launch_beam_reorder(states, n, parents, lengths, groups, beams, h->flags, s));
+  const cudaError_t e = kld::launch_beam_reorder(states, n, parents, lengths, groups, beams, h->flags, s);
+  if (e == cudaErrorInvalidConfiguration) return KLD_ERR_INVALID_ARG;  // more runs than a grid holds
+  KLD_CUDA(e);
   return mark_done(h, s);
 }
 

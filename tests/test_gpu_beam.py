@@ -15,7 +15,7 @@ import torch
 
 import packed_ref
 from logit_kl_divergence_b200 import (BEAM_BAD_PARENT, BEAM_BAD_SCORE, BEAM_NONFINITE, BeamSearch,
-                                      KLDError, KLDStats, PackedLogits, pack_logits)
+                                      KLDError, KLDStats, PackedLogits, _lib, pack_logits)
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -344,3 +344,23 @@ def test_outputs_over_inputs_are_refused():
         done = torch.zeros((2, 2), dtype=torch.bool, device=DEV)
         assert beam.select(x, scores, 2, finished=done, eos=3, out=tuple(free))[0] is free[0]
         assert beam.status() == 0
+
+
+def test_reorder_refuses_states_that_overlap_and_runs_past_a_grid():
+    kv = torch.arange(4 * 3 * 2 * 5 * 8, dtype=torch.float32, device=DEV).view(4, 3, 2, 5, 8)
+    parents = torch.tensor([[1, 0, 3, 3]], dtype=torch.int32, device=DEV)
+    with BeamSearch(1, 4, device=DEV) as beam:
+        for states in ([kv, kv], [(kv[:, :, 0], 2), (kv[:, :, 0, 1:], 2)], [kv, (kv[:, 1, 1], 1)]):
+            with pytest.raises(ValueError):
+                beam.reorder(states, parents)
+        want = packed_ref.reorder(kv.cpu().numpy(), parents.cpu().numpy())
+        beam.reorder([(kv[:, :, 0], 2), (kv[:, :, 1], 2)], parents,
+                     torch.full((4,), 1 << 30, dtype=torch.int32, device=DEV))
+        assert np.array_equal(kv.cpu().numpy(), want)
+        # more runs than one launch takes: refused before the first state is moved
+        many = [_lib.State(kv.data_ptr(), 960, 1, 0, 1, 960, 0, 0),
+                _lib.State(kv.data_ptr(), 1 << 47, (1 << 31) - 1, 4096, 1, 2048 * 16, 0, 0)]
+        many[1].outer_stride = 2048 * 16
+        status = beam._lib.kld_beam_reorder(beam._h, (_lib.State * 2)(*many), 2, parents.data_ptr(), None, 1, 4, None)
+        assert status == _lib.KLD_ERR_INVALID_ARG
+        assert np.array_equal(kv.cpu().numpy(), want) and beam.status() == 0

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from logit_kl_divergence_b200 import _lib, PackedLogits, pack_logits
-from logit_kl_divergence_b200.beam import BeamStates, _describe
+from logit_kl_divergence_b200.beam import BeamStates, _apart, _describe, _span
 
 INVALID, DTYPE = _lib.KLD_ERR_INVALID_ARG, _lib.KLD_ERR_DTYPE
 P = 1 << 20
@@ -125,3 +125,23 @@ def test_bound_states_are_checked():
         BeamStates([torch.zeros((2, 3))], torch.device("cpu"))  # not CUDA tensors
     with pytest.raises(ValueError):
         BeamStates([torch.zeros((2, 3)), torch.zeros((3, 3))], torch.device("cpu"))
+
+
+def test_states_that_share_memory_are_told_from_those_that_interleave():
+    def pair(x, y, dx=None, dy=None):
+        x, y = _Cuda(x), _Cuda(y)
+        return _apart((_span(x), _describe(x, dx), x.shape[0]), (_span(y), _describe(y, dy), y.shape[0]))
+
+    kv = torch.zeros((6, 3, 2, 10, 4))       # rows, heads, k or v, time, dim
+    assert pair(kv[:, :, 0], kv[:, :, 1], 2, 2) and pair(kv[:, 0, 0], kv[:, 1, 1], 1, 1)
+    assert pair(kv[:, 0], kv[:, 1:], 2, None) and pair(kv[:3], kv[3:], 3, 3)
+    assert not pair(kv[:, :, 0], kv[:, :, 0], 2, 2) and not pair(kv[:, :, 0, :6], kv[:, :, 0, 4:], 2, 2)
+    assert pair(kv[:, :, 0, :6], kv[:, :, 0, 6:], 2, 2) and not pair(kv, kv[:, 2], 3, 2)
+    assert not pair(kv[:, :, 0], kv[:, 0, 0], 2, 1) and not pair(kv[:4], kv[1:5], 3, 3)
+    one = kv[:1]
+    assert pair(one[:, :, 0], one[:, :, 1], 2, 2) and not pair(one[:, :, 0], one[:, :, 0, 1:], 2, 2)
+    t = torch.zeros((3, 6, 2, 10, 4)).transpose(0, 1)  # rows between the runs of a head
+    assert pair(t[:, :, 0], t[:, :, 1], 2, 2) and not pair(t[:, :, 0], t[:, :, 0, 2:], 2, 2)
+    flat = torch.zeros(64)
+    assert not pair(flat[:60].view(6, 10), flat[4:64].view(12, 5)[:6])
+    assert pair(flat[:30].view(6, 5), flat[30:60].view(6, 5))
