@@ -364,3 +364,38 @@ def test_reorder_refuses_states_that_overlap_and_runs_past_a_grid():
         status = beam._lib.kld_beam_reorder(beam._h, (_lib.State * 2)(*many), 2, parents.data_ptr(), None, 1, 4, None)
         assert status == _lib.KLD_ERR_INVALID_ARG
         assert np.array_equal(kv.cpu().numpy(), want) and beam.status() == 0
+
+
+@pytest.mark.parametrize("groups,beams,v,k", [(1, 1, 1000003, 128), (1, 64, 9001, 128), (600, 4, 130, 64),
+                                              (2500, 1, 5000, 1), (3, 1, 257, 128)])
+def test_many_and_few_lists(groups, beams, v, k):
+    _check(_rows(groups * beams, v, k), _scores(groups, beams, k), k)
+
+
+def test_lists_that_overflow_among_many_parts():
+    x = _rows(8, 200000, 12)
+    x[0] = 1.0                                     # one value everywhere
+    x[1, ::2] = 12.0                               # half of the row at the maximum
+    x[2] = torch.arange(200000).float() * 1e-4     # rising: every entry passes the bound before it
+    x[3, 150000:] = 12.0
+    for dt in (torch.float32, torch.bfloat16):
+        _check(x.to(dt), _scores(2, 4, 2), 100)
+        _check(x.to(dt), torch.zeros((1, 8)), 128)
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows 2^28 elements apart: the last ones lie past 2^31 elements."""
+    groups, beams, v, ld = 3, 3, 3000, 1 << 28
+    x = _rows(groups * beams, v, 21).bfloat16()
+    flat = torch.empty((groups * beams - 1) * ld + v, dtype=torch.bfloat16, device=DEV)
+    view = torch.as_strided(flat, (groups * beams, v), (ld, 1))
+    view.copy_(x)
+    _check(x, _scores(groups, beams, 21), 6, logits=view)
+    cache = torch.as_strided(flat, (groups * beams, 50, 8), (ld, 8, 1))
+    cache.copy_(torch.arange(groups * beams * 400).view(groups * beams, 50, 8).remainder(251).bfloat16())
+    parents = torch.tensor([[1, 0, 0], [2, 2, 1], [0, 1, 1]], dtype=torch.int32)
+    lengths = torch.tensor([50, 7, 0, 1, 50, 9, 13, 3, 90], dtype=torch.int32)
+    want = packed_ref.reorder(cache.float().cpu().numpy(), parents.numpy(), lengths.numpy(), 1)
+    with BeamSearch(groups, beams, device=DEV) as beam:
+        beam.reorder([(cache, 1)], parents.to(DEV), lengths.to(DEV))
+        assert np.array_equal(cache.float().cpu().numpy(), want) and beam.status() == 0

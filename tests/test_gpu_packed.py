@@ -375,3 +375,52 @@ def test_outputs_over_inputs_are_refused():
                                tok, out=at(byte, torch.bfloat16, n, v))
         st.run_grad_packed(base, quant, tok, out=quant)
         st.result()
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+@pytest.mark.parametrize("n,v", [(1, 900001), (7, 300000), (800, 41000)])
+def test_masks_in_every_block(n, v, quant):
+    """Every chunk holds masked entries: more of them than a warp lists."""
+    b, q, tok = _pair(n, v, n)
+    for x in (b, q):
+        x[:, 5::97] = -math.inf
+    b[:, 40::1009] = -math.inf          # and some in the base only
+    tok = torch.full((n,), 4, dtype=torch.int32)
+    _check(b, q, tok, "f32" if quant == "packed" else quant, "bf16", scale=2.0, pack_quant=quant == "packed")
+
+
+def test_bad_and_empty_rows_among_many():
+    n, v = 1500, 515
+    b, q, tok = _pair(n, v, 5)
+    b[::7] = -math.inf
+    q[3::11] = -math.inf
+    q[5::13, 17] = math.nan
+    b[6::17, ::2] = -math.inf           # finite quant entries there
+    tok[::5] = v
+    tok[1::5] = -7
+    _check(b, q, tok, "bf16", "f32")
+    _check(b, q, tok, "f32", "f32", pack_quant=True)
+
+
+def test_rows_longer_than_32_bit_offsets():
+    """70 rows of 2^25 + 1 columns: offsets past 2^31 in codes and logits."""
+    n, v = 70, (1 << 25) + 1
+    q = torch.zeros((n, v), dtype=torch.bfloat16, device=DEV)
+    q[:, 77] = 3.0
+    q[n - 1, v - 1] = 9.0
+    base = pack_logits(q)
+    # a block of one value has code 1 whatever the value; its header tells
+    assert base.codes[n - 1, v - 1] == 1 and base.heads[n - 1, -1] != base.heads[n - 1, 1]
+    assert base.unpack(torch.bfloat16)[n - 1, v - 3:].tolist() == [0.0, 0.0, 9.0]
+    other = q.clone()
+    other[n - 1, v - 1] = 0.0
+    tok = torch.full((n,), 77, dtype=torch.int32, device=DEV)
+    with KLDStats(n, device=DEV) as st:
+        g, rows = st.run_grad_packed(base, other, tok, per_row=True)
+        assert (rows["kld"][:n - 1] == 0).all() and (g[:n - 1] == 0).all()
+        z_b, z_q = v - 2 + math.exp(3.0) + math.exp(9.0), v - 1 + math.exp(3.0)
+        kl = 9.0 * math.exp(9.0) / z_b - math.log(z_b) + math.log(z_q)
+        assert abs(rows["kld"][n - 1].item() - kl) <= 1e-6 + 1e-4 * kl
+        assert rows["amax_b"][n - 1] == v - 1 and (rows["amax_q"] == 77).all()
+        want = 1.0 / z_q - math.exp(9.0) / z_b
+        assert abs(g[n - 1, v - 1].item() - want) <= 2.0 ** -8 * abs(want) + 4e-6 * (1.0 / z_q + math.exp(9.0) / z_b)
