@@ -456,8 +456,8 @@ kld_status_t kld_stats_run_packed(kld_stats_t h, const kld_packed_t* base, const
  * kld_stats_run_grad with the base rows (and the quant rows, when
  * quant_packed is set) read from checkpoints: the same statistic plus
  *   grad[i][j] = scale * (softmax(q_i)_j - softmax(b_i)_j)
- * of the restored values, zero on excluded rows, in one kernel that reads
- * the rows once. grad: caller-owned DEVICE memory, [N, V] of grad_dtype,
+ * of the restored values, zero on excluded rows, in one kernel (its second
+ * look at a row finds what is still on the chip). grad: caller-owned DEVICE memory, [N, V] of grad_dtype,
  * aligned to its element size; it may be the dense quant rows themselves when
  * grad_dtype is quant_dtype, and may not overlap the inputs otherwise. A
  * non-finite scale is KLD_ERR_INVALID_ARG.

@@ -192,8 +192,7 @@ class KLDStats:
                         per_row: bool = False, stream=None):
         """:meth:`run_packed` plus the gradient with respect to the quant
         logits, as :meth:`run_grad` gives it (``grad_dtype``: the quant
-        logits' by default, float32 for packed ones), from one read of the
-        rows; ``out`` may be the dense quant tensor itself. Returns the gradient, or (gradient, rows) with ``per_row``.
+        logits' by default, float32 for packed ones), in one kernel; ``out`` may be the dense quant tensor itself. Returns the gradient, or (gradient, rows) with ``per_row``.
         Asynchronous on the stream."""
         head, fields, rows, s = self._packed_call(base, quant, token_ids, per_row, stream)
         if out is None:

@@ -1,7 +1,7 @@
 // kld_packed_rows.cu -- the statistic and the gradient with packed base rows
 // (mathematics: kld_packed_rows.cuh).
 //
-// One read of the logits for both passes. A row belongs to one CTA of four
+// Both passes in one launch. A row belongs to one CTA of four
 // warps, or, when there are few rows, to a cluster of 2, 4 or 8 of them, each
 // taking a run of its 512-column chunks. A warp streams its chunks, two at a
 // time, through shared-memory slots of its own with cp.async (every global
@@ -9,12 +9,13 @@
 // registers. After the sums are merged (every warp leaves its sums in the
 // shared memory of all of the cluster's CTAs, one cluster barrier) the
 // gradient pass walks the chunks backwards: those still in their slots are
-// not read again, the others come back from L2. No wait in this kernel
-// depends on another launch.
+// not read again, the others come from L2 while the rows in flight fit there
+// (740 rows of 151936 bf16 do not: 863 MB read for 472 MB of rows, at half of
+// HBM's rate). No wait in this kernel depends on another launch.
 //
-// Bound by instruction issue: 20.5 warp instructions an element for the
-// statistic, 13 more for the gradient, at 65-70 % of the issue slots (the
-// rest are the row's serial ends). Five CTAs of 128 threads and 96 registers
+// Bound by instruction issue: 20 thread instructions an element for the
+// statistic, 13 more for the gradient, at 60-70 % of the issue slots (the
+// rest are the rows' serial ends and the last wave). Five CTAs of 128 threads and 96 registers
 // an SM measured best for the statistic of 8192 x 151936 bf16 (1.04 ms; 64
 // threads 1.18, 256 threads 1.20, 512 threads 1.59 ms); so did two chunks at
 // a time (one: 1.10 ms). Clusters for many rows cost more ends than they save
