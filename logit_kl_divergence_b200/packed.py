@@ -21,9 +21,16 @@ PACK_BLOCK = _lib.KLD_PACK_BLOCK
 _DTYPES = {torch.float32: _lib.KLD_F32, torch.bfloat16: _lib.KLD_BF16, torch.float16: _lib.KLD_F16}
 
 
+# The current stream's handle by device index: 0.2 us, where the Stream object
+# that torch.cuda.current_stream builds takes 2.5 us, a seventh of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on(stream, device) -> int:
     """The handle of the stream to launch on."""
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     if stream.device != device:
         raise ValueError("the stream must be on the tensors' device")
@@ -62,10 +69,14 @@ class PackedLogits:
             raise ValueError("codes and heads must be on one device")
         if codes.data_ptr() % 16:
             raise ValueError("codes must be aligned to 16 bytes")
+        self._hold(codes, heads, vocab)
+
+    def _hold(self, codes: torch.Tensor, heads: torch.Tensor, vocab: int) -> "PackedLogits":
         self.codes, self.heads, self.vocab = codes, heads, vocab
         self.shape = (codes.shape[0], vocab)
         self.device = codes.device
         self._c = _lib.Packed(codes.data_ptr(), heads.data_ptr())
+        return self
 
     @classmethod
     def empty(cls, n_rows: int, vocab: int, device=None) -> "PackedLogits":
@@ -127,9 +138,10 @@ def pack_logits(logits: torch.Tensor, out: PackedLogits | None = None, stream=No
     s = _on(stream, logits.device)
     if out is None:
         n, blocks = logits.shape[0], -(-logits.shape[1] // PACK_BLOCK)
-        out = PackedLogits(_empty(stream, (n, blocks * PACK_BLOCK), torch.uint8, logits.device),
-                           _empty(stream, (n, blocks), torch.int32, logits.device), logits.shape[1])
-    if out.shape != tuple(logits.shape) or out.device != logits.device:
+        out = PackedLogits.__new__(PackedLogits)._hold(  # made to fit: no checks
+            _empty(stream, (n, blocks * PACK_BLOCK), torch.uint8, logits.device),
+            _empty(stream, (n, blocks), torch.int32, logits.device), logits.shape[1])
+    elif out.shape != tuple(logits.shape) or out.device != logits.device:
         raise ValueError("out must hold as many rows and columns on the logits' device")
     if len(out):
         _lib.check(lib.kld_pack_logits(logits.data_ptr(), logits.shape[0], logits.shape[1],
