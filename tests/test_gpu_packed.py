@@ -424,3 +424,17 @@ def test_rows_longer_than_32_bit_offsets():
         assert rows["amax_b"][n - 1] == v - 1 and (rows["amax_q"] == 77).all()
         want = 1.0 / z_q - math.exp(9.0) / z_b
         assert abs(g[n - 1, v - 1].item() - want) <= 2.0 ** -8 * abs(want) + 4e-6 * (1.0 / z_q + math.exp(9.0) / z_b)
+
+
+def test_ties_go_to_even_whatever_the_base():
+    """Blocks whose values lie halfway between two steps, at odd and even
+    bases of either sign; some with masked entries between."""
+    k = torch.arange(128).float()
+    rows = []
+    for base in (-300, -7, -4, 0, 1, 2, 1001, 4096):
+        rows.append((base + 2 * k + torch.where(k % 3 == 0, 0.0, 0.5)).clone())  # range 254: steps of one
+        x = rows[-1].clone()
+        x[5::9] = -math.inf
+        rows.append(x)
+    _check_pack(torch.stack(rows))
+    _check_pack(torch.cat(rows).view(2, -1)[:, :1019].contiguous())
