@@ -549,7 +549,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
   };
   if (places <= kStep) read(tid);
   offer_all();
-  if (sh.list.count > kThreads) {
+  // Read by all before a finished beam's push may raise it: the branch holds
+  // barriers, so every thread has to take the same side of it.
+  const int offered = sh.list.count;
+  __syncthreads();
+  if (offered > kThreads) {
     // Few lists for k, or long ones: a closer bound from their entries (a
     // list holds at least k, or all its part has).
     best = neg_inf();

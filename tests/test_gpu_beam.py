@@ -399,3 +399,23 @@ def test_rows_past_32_bit_offsets():
     with BeamSearch(groups, beams, device=DEV) as beam:
         beam.reorder([(cache, 1)], parents.to(DEV), lengths.to(DEV))
         assert np.array_equal(cache.float().cpu().numpy(), want) and beam.status() == 0
+
+
+@pytest.mark.parametrize("entries", [225, 240, 255, 256, 257, 288])
+def test_finished_beams_at_the_merge_s_list_limit(entries):
+    """So many entries that tie at the top of 32 live beams, and 32 finished
+    beams that join them: the merge decides at 256 entries whether to look for
+    a closer bound, before the finished beams' entries come in."""
+    groups, beams, v, k = 4, 64, 333, 128
+    x = torch.full((groups * beams, v), -math.inf)
+    done = torch.zeros((groups, beams), dtype=torch.bool)
+    done[:, 1::2] = True
+    for g in range(groups):
+        for i in range(entries):  # equal rows as far as they go
+            x[g * beams + 2 * (i % 32), (7 * (i // 32)) % v] = 1.0
+    s = torch.full((groups, beams), -2.0)
+    s[:, 1::2] -= torch.arange(32) * 0.125
+    with BeamSearch(groups, beams, max_k=k, device=DEV) as beam:
+        for _ in range(20):
+            _check(x, s, k, finished=done, eos=5, beam=beam)
+        assert beam.status() == 0
