@@ -336,6 +336,10 @@ Shape shape_for(int64_t N, int64_t V, int sm_count) {
   constexpr int most = (228 * 1024 / kCtasPerSm - static_cast<int>(sizeof(Shared)) - 1024) /
                        (kWarps * kSub * Slot<QT>::kBytes);
   static_assert(most >= kDepth, "slots");
+  // What any kernel may use without an attribute of the function, which all
+  // host threads would share.
+  static_assert(most * kWarps * kSub * Slot<QT>::kBytes + static_cast<int>(sizeof(Shared)) <= 48 * 1024,
+                "shared memory of a CTA");
   const int64_t chunks = (V + kChunk - 1) / kChunk + 1;
   // Few rows are split as long as all CTAs run at once (and a warp has more
   // than one chunk): 16 x 262144 fp32 87 us whole, 43 us in eight; 512 x 32003
@@ -355,8 +359,6 @@ cudaError_t launch_shape(const Operands& in, const Outputs& out, int sm_count, c
   const Shape sh = shape_for<QT>(in.N, in.V, sm_count);
   const int smem = kWarps * sh.slots * kSub * Slot<QT>::kBytes;
   auto kern = kld_packed_rows_kernel<QT, OT, kOff>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(in.N * sh.cluster));
   cfg.blockDim = dim3(kThreads);

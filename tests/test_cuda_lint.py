@@ -34,3 +34,13 @@ def test_the_check_catches_the_pattern():
     assert SHORT_CIRCUIT.search("x = c ? __shfl_sync(0xffffffffu, v, 0) : 0;")
     assert not SHORT_CIRCUIT.search("const bool direct = !__all_sync(0xffffffffu, axl <= kTau);")
     assert not SHORT_CIRCUIT.search("if (__any_sync(0xffffffffu, a || b)) {")
+
+
+def test_the_packed_rows_kernels_set_no_attribute_for_a_launch():
+    """A kernel's largest dynamic shared memory is state of the function that
+    all host threads share: set to one call's need, it can stand too small for
+    another thread's call between its setting and its launch. These kernels
+    stay within what needs no attribute (asserted where they are launched)."""
+    for name in ("kld_packed_rows.cu", "kld_packed_rows.cuh"):
+        with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+            assert "cudaFuncSetAttribute" not in _code(f.read()), name

@@ -18,6 +18,7 @@ rounding 2^-24: <= 3.5e-6 together. Outputs in 16 bits add half a step, 2^-8
 (bf16) or 2^-11 (fp16) of the value, and fp16's fixed step 2^-25 below its
 normal range."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -438,3 +439,31 @@ def test_ties_go_to_even_whatever_the_base():
         rows.append(x)
     _check_pack(torch.stack(rows))
     _check_pack(torch.cat(rows).view(2, -1)[:, :1019].contiguous())
+
+
+def test_two_host_threads_with_handles_of_their_own():
+    """Calls that need different amounts of shared memory of the same kernel,
+    from two host threads at once, each with its own handle and stream."""
+    sizes = [(2, 900), (2, 60000), (2, 3000), (2, 30000)]
+    errors = []
+
+    def work(i, n, v):
+        try:
+            b, q, _ = _pair(n, v, v)
+            side = torch.cuda.Stream(DEV)
+            with torch.cuda.stream(side), KLDStats(n, DEV) as st:
+                base = pack_logits(b.to(DEV))
+                quant = pack_logits(q.to(DEV))
+                want = st.run_packed(base, quant, per_row=True)["kld"].clone()
+                for _ in range(1500):
+                    got = st.run_packed(base, quant, per_row=True)["kld"]
+                assert torch.equal(got, want)
+        except Exception as e:
+            errors.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i, *s)) for i, s in enumerate(sizes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
