@@ -13,7 +13,9 @@
 // One exponential an element; e^x - 1 - x is x^2 times a polynomial for
 // |x| <= 2.5 (three degrees by the warp's largest |x|). Steps of a warp that hold
 // a larger or non-finite x take a second exponential, h_j = e_j e^x_j, and sum
-// it apart (Q, with their e in D), so B = A + C over the others plus Q - D.
+// it apart (Q, with their e in D), so B = A + C over the others plus Q - D. Q
+// is summed as 2^(q_j L - G) in a frame G near those steps' quant maximum: in
+// the base row's frame an argument of 100 would be rounded by 4e-6.
 // Nothing of the size of KL is got by subtracting rounded exponentials, so
 // rows that are nearly equal or nearly one-hot keep their accuracy, and so do
 // rows whose two distributions hardly meet. F and K belong to a
@@ -358,11 +360,12 @@ __device__ __forceinline__ void step_global(const RowPtr& rp, int64_t V, int c, 
 struct Part {
   float F, K;      // frame (a whole number; kNoFrame before any value), centre
   float S, A, C;   // over the polynomial steps
-  float D, E, Q;   // over the others: sums of e, e x, h
+  float D, E;      // over the others: sums of e, e x
+  float G, Q;      // and of 2^(q L - G), G their quant exponentials' frame
   float mb, mq;    // maxima of its columns
   int tb, tq;      // the first of the warp's chunks that hold them
 };
-constexpr int kPartWords = 12;
+constexpr int kPartWords = 13;
 static_assert(sizeof(Part) == 4 * kPartWords, "Part is stored word by word");
 
 // The row's merged sums and what the gradient pass needs of them.
@@ -389,15 +392,14 @@ struct State {
   float F, K, T;  // T: a value above it moves the frame and the centre
   int form;       // order of the log-ratio's roundings (ratio_form)
   f2 S, A, C;     // pairs of fp32
-  float D, E, Q;
+  float D, E, G, Q;
   float mb, mq;
   int ib, iq;
 };
 
 // Moves a warp's frame to its step's maximum M (um: the lane's own), rebasing
 // the lanes' sums exactly in F and by
-//   A' = A + d S,  C' = e^d C + (e^d - 1) A + (e^d - 1 - d) S,
-//   E' = E + d D,  Q' = e^d Q
+//   A' = A + d S,  C' = e^d C + (e^d - 1) A + (e^d - 1 - d) S,  E' = E + d D
 // in K (d its change).
 template <int QT>
 __device__ __forceinline__ void raise(State& s, const float* b, const float* q, const uint32_t* qw,
@@ -438,7 +440,6 @@ __device__ __forceinline__ void raise(State& s, const float* b, const float* q, 
     s.C = pk(C[0], C[1]);
     s.E = sc * (s.E + d * s.D);
     s.D *= sc;
-    s.Q = sc * (s.Q + e1 * s.Q);
   }
   s.F = F;
   s.K = K;
@@ -508,6 +509,11 @@ __device__ __forceinline__ bool add_step(State& s, const float* b, const float* 
     // Large or non-finite log-ratios. A masked base entry has e = 0 and gives
     // its h to Q; x = -inf with a base entry above -inf makes E non-finite,
     // which sends the row to slow_row.
+    const float G = floorf(warp_max(mq) * kLog2e);
+    if (G > s.G) {
+      s.Q *= static_cast<float>(pow2d(s.G - G));
+      s.G = G;
+    }
     float D = 0.f, E = 0.f, Q = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -519,7 +525,7 @@ __device__ __forceinline__ bool add_step(State& s, const float* b, const float* 
         const float e = ex2(fmaf(bk, kLog2e, -s.F));
         D += e;
         E += bk == neg_inf() ? 0.f : e * xs[h];
-        Q += ex2(fmaf(q_el<kPk>(q, qw, 2 * k + h) + s.K, kLog2e, -s.F));
+        Q += ex2(fmaf(q_el<kPk>(q, qw, 2 * k + h), kLog2e, -s.G));
       }
     }
     s.D += D;
@@ -551,6 +557,7 @@ __device__ __forceinline__ Part part_of(const State& s) {
   w.C = sum_lanes(v0 + v1);
   w.D = sum_lanes(s.D);
   w.E = sum_lanes(s.E);
+  w.G = s.G;
   w.Q = sum_lanes(s.Q);
   w.mb = warp_max(s.mb);
   w.mq = warp_max(s.mq);
@@ -566,6 +573,7 @@ __device__ __forceinline__ State fresh_state() {
   s.form = 0;
   s.S = s.A = s.C = splat(0.f);
   s.D = s.E = s.Q = 0.f;
+  s.G = kNoFrame;
   s.mb = s.mq = neg_inf();
   s.ib = s.iq = 0;
   return s;
@@ -642,7 +650,9 @@ __device__ __noinline__ void merge(const Part* part, int parts, float scale, Tot
   double S = 0.0, A = 0.0, C = 0.0, D = 0.0, E = 0.0, Q = 0.0;
   for (int i = lane; i < parts; i += 32) {
     const Part p = part[i];
-    if (p.S == 0.f && p.D == 0.f && p.E == 0.f && p.Q == 0.f) continue;
+    if (p.Q != 0.f)  // from its frame to the row's: 2^(F - K L) is the unit there
+      Q += p.Q * exp2(static_cast<double>(p.G) - static_cast<double>(F) + static_cast<double>(K) * kLog2eD);
+    if (p.S == 0.f && p.D == 0.f && p.E == 0.f) continue;
     const double sc = pow2d(p.F - F);
     const double d = static_cast<double>(K) - static_cast<double>(p.K);
     double e1 = 0.0, phi = 0.0;
@@ -656,7 +666,6 @@ __device__ __noinline__ void merge(const Part* part, int parts, float scale, Tot
     C += sc * (c + e1 * c + e1 * kLambda * a + phi * s);
     D += sc * p.D;
     E += sc * (p.E + d * p.D);
-    Q += sc * (p.Q + e1 * p.Q);
   }
   S = warp_sum(S);
   A = warp_sum(A);

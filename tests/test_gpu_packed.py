@@ -467,3 +467,31 @@ def test_two_host_threads_with_handles_of_their_own():
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+def _peaked(n, v, peak, gap):
+    """A token that the base model puts first and the quant rows hold `gap`
+    nats below their own maximum (a token banned by a bias), which is in the
+    same chunk, another warp's, or another CTA's of the cluster."""
+    g = torch.Generator().manual_seed(v + int(gap))
+    b = torch.randint(-4, 5, (n, v), generator=g) * 0.125
+    q = torch.randint(-4, 5, (n, v), generator=g) * 0.125
+    b[:, 5], q[:, 5], q[:, peak] = 30.0, 30.0 - gap, 30.0
+    return b, q
+
+
+PEAKS = [(1, 2048, 300), (1, 8192, 1500), (1, 70001, 60000), (900, 2048, 1500)]
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+@pytest.mark.parametrize("gap", [40.0, 85.0, 95.0, 100.0, 300.0])
+@pytest.mark.parametrize("n,v,peak", PEAKS)
+def test_statistic_of_quant_rows_that_peak_far_from_the_base_argmax(n, v, peak, gap, quant):
+    b, q = _peaked(n, v, peak, gap)
+    _check(b, q, torch.full((n,), 9, dtype=torch.int32), "f32" if quant == "packed" else quant,
+           pack_quant=quant == "packed")
+    # the peak's own NLL, about e^-25, at the bar of a row
+    base, quant = pack_logits(b.to(DEV)), q.to(DEV) if quant != "packed" else pack_logits(q.to(DEV))
+    with KLDStats(n, DEV) as st:
+        rows = st.run_packed(base, quant, torch.full((n,), peak, dtype=torch.int32, device=DEV), per_row=True)
+        assert (rows["nll"].abs() <= 1e-6).all()
