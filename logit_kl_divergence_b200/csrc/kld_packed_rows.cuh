@@ -373,8 +373,11 @@ struct Total {
   double S, A, B, q;  // sum of e, e x, e (e^x - 1), e e^x over all steps
   float F, K;
   float mb, mq;
-  float Fq;        // frame of the quant row's exponentials
-  float cb, cq;    // scale / (their sums in the frames)
+  // The gradient's frames, floor(log2) of the rows' whole sums, so that its
+  // exponentials are the softmax values within a factor of two wherever the
+  // rows peak; scale / (the sums in them), in (scale / 2, scale]. The two are
+  // formed alike: equal rows give equal values.
+  float Fb, Fq, cb, cq;
   int good;
 };
 
@@ -685,11 +688,13 @@ __device__ __noinline__ void merge(const Part* part, int parts, float scale, Tot
     t.mq = mq;
     t.good = t.S > 0.0 && t.S < 1e300 && fabs(t.A) < 1e300 && t.q > 0.0 && t.q < 1e300 &&
              fabsf(F) < 1e6f && fabsf(K) < 1e6f;
-    // sum_j 2^(q_j L) = t.q 2^(F - K L): its whole part is the quant row's frame
-    const double at = static_cast<double>(F) - static_cast<double>(K) * kLog2eD;
-    t.Fq = static_cast<float>(floor(at));
-    t.cb = static_cast<float>(scale / t.S);
-    t.cq = static_cast<float>(scale / (t.q * exp2(at - floor(at))));
+    // sum_j 2^(b_j L) = t.S 2^F, sum_j 2^(q_j L) = t.q 2^(F - K L)
+    const double lb = log2(t.S) + static_cast<double>(F);
+    const double lq = log2(t.q) + static_cast<double>(F) - static_cast<double>(K) * kLog2eD;
+    t.Fb = static_cast<float>(floor(lb));
+    t.Fq = static_cast<float>(floor(lq));
+    t.cb = static_cast<float>(scale * exp2(floor(lb) - lb));
+    t.cq = static_cast<float>(scale * exp2(floor(lq) - lq));
     *total = t;
   }
 }
@@ -839,12 +844,12 @@ __device__ void write_row(const Outputs& out, const Token& tok, int64_t r, doubl
 
 // What the gradient of a row needs of its sums.
 struct GradScale {
-  float F, Fq, cb, cq;
-  __device__ __forceinline__ explicit GradScale(const Total& t) : F(t.F), Fq(t.Fq), cb(t.cb), cq(t.cq) {}
+  float Fb, Fq, cb, cq;
+  __device__ __forceinline__ explicit GradScale(const Total& t) : Fb(t.Fb), Fq(t.Fq), cb(t.cb), cq(t.cq) {}
 };
 // The gradient of 16 columns (into b).
 __device__ __forceinline__ void grad_values(const GradScale& t, float* b, const float* q) {
-  const f2 L2 = splat(kLog2e), fb = splat(-t.F), fq = splat(-t.Fq);
+  const f2 L2 = splat(kLog2e), fb = splat(-t.Fb), fq = splat(-t.Fq);
   const f2 cb2 = splat(t.cb), cq2 = splat(t.cq), zero2 = splat(0.f);
 #pragma unroll
   for (int k = 0; k < 16; k += 2) {

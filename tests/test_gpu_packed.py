@@ -495,3 +495,13 @@ def test_statistic_of_quant_rows_that_peak_far_from_the_base_argmax(n, v, peak, 
     with KLDStats(n, DEV) as st:
         rows = st.run_packed(base, quant, torch.full((n,), peak, dtype=torch.int32, device=DEV), per_row=True)
         assert (rows["nll"].abs() <= 1e-6).all()
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+@pytest.mark.parametrize("gap", [40.0, 85.0, 95.0, 100.0, 300.0])
+@pytest.mark.parametrize("n,v,peak", PEAKS)
+def test_gradient_of_quant_rows_that_peak_far_from_the_base_argmax(n, v, peak, gap, quant):
+    b, q = _peaked(n, v, peak, gap)
+    tok = torch.full((n,), 9, dtype=torch.int32)
+    for scale in (1.0, 1.0 / 2048):
+        _check(b, q, tok, "f32" if quant == "packed" else quant, "f32", scale=scale, pack_quant=quant == "packed")
