@@ -202,46 +202,79 @@ struct SelectShared {
   uint32_t choice[kMaxLists];       // beam << 16 | list
 };
 
-// Column j of a row, -inf outside.
+// Column j of a row, -inf from j1 on.
 template <int DT>
-__device__ __forceinline__ float value_at(const char* row, int64_t j, int64_t V) {
-  return j >= 0 && j < V ? Type<DT>::load(row + j * Type<DT>::kBytes) : neg_inf();
+__device__ __forceinline__ float value_at(const char* row, int64_t j, int64_t j1) {
+  return j < j1 ? Type<DT>::load(row + j * Type<DT>::kBytes) : neg_inf();
 }
 
-// A tile: each thread NV vectors of 16 bytes, vector v of thread t being the
-// tile's (v * kThreads + t)-th.
+// A row and what its reading needs: the bytes it starts past a 16-byte
+// boundary, and the matrix's first and last byte (whole 16-byte vectors that
+// lie between them may be read).
+struct Row {
+  const char* p;
+  uint32_t mis;
+  const char *begin, *end;
+};
+
+// A tile: each thread NV vectors of E columns, vector v of thread t being the
+// tile's (v * kThreads + t)-th from the row's start on. Rows that start
+// inside a 16-byte vector are read as the two vectors that hold one of
+// theirs, shifted into place: so the columns that a thread sums do not depend
+// on where the row lies, and equal rows have equal sums (on the memory's own
+// grid their log-sum-exps differed by 1e-8, which broke ties between beams).
 template <int DT>
 struct Tile {
   static constexpr int E = 16 / Type<DT>::kBytes;
   static constexpr int NV = kPer / E;
   uint32_t w[4 * NV];
-  __device__ void load(const char* row, int64_t j0, int64_t j1, int64_t V, int off) {
-    // columns [j0, j1) of the vector grid, which starts `off` columns before the row
-    constexpr int64_t kCols = static_cast<int64_t>(kThreads) * kPer;
-    if (j0 >= off && j0 + kCols <= j1 && j0 - off + kCols <= V) {  // the whole tile, for all threads
-      const uint4* p = reinterpret_cast<const uint4*>(row + (j0 - off) * Type<DT>::kBytes) + threadIdx.x;
+  // 16 bytes from p on, p mis past a boundary, as they lie in memory.
+  __device__ __forceinline__ static void shifted(const char* p, uint32_t mis, uint32_t* to) {
+    const uint4* a = reinterpret_cast<const uint4*>(p - mis);
+    uint32_t x[8];
+    *reinterpret_cast<uint4*>(x) = __ldg(a);
+    *reinterpret_cast<uint4*>(x + 4) = __ldg(a + 1);
+    packed::shift_bytes<4, DT == KLD_F32>(x, mis);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(p + v * kThreads);
-      return;
+    for (int k = 0; k < 4; ++k) to[k] = x[k];
+  }
+  // Columns [j0, j0 + tile) of the row, -inf from j1 on.
+  __device__ void load(const Row& row, int64_t j0, int64_t j1) {
+    constexpr int64_t kCols = static_cast<int64_t>(kThreads) * kPer;
+    constexpr int kVec = kThreads * 16;  // bytes from one vector of a thread to its next
+    const char* tile = row.p + j0 * Type<DT>::kBytes;
+    const char* at = tile + threadIdx.x * 16;
+    if (j0 + kCols <= j1) {  // the whole tile, for all threads
+      if (row.mis == 0) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(reinterpret_cast<const uint4*>(at + v * kVec));
+        return;
+      }
+      if (tile - row.mis >= row.begin && tile + NV * kVec + 16 - row.mis <= row.end) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) shifted(at + v * kVec, row.mis, &w[4 * v]);
+        return;
+      }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t g = j0 + (v * kThreads + static_cast<int>(threadIdx.x)) * E;
-      const int64_t j = g - off;
-      uint4 x;
-      if (g < j1 && j >= 0 && j + E <= V) {
-        x = __ldcs(reinterpret_cast<const uint4*>(row + j * Type<DT>::kBytes));
+      const int64_t j = j0 + (v * kThreads + static_cast<int>(threadIdx.x)) * E;
+      const char* p = at + v * kVec;
+      if (j + E <= j1 && row.mis == 0) {
+        *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(reinterpret_cast<const uint4*>(p));
+      } else if (j + E <= j1 && p - row.mis >= row.begin && p + 32 - row.mis <= row.end) {
+        shifted(p, row.mis, &w[4 * v]);
       } else {
         float y[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) y[k] = g < j1 ? value_at<DT>(row, j + k, V) : neg_inf();
-        x = Type<DT>::vec(y);
+        for (int k = 0; k < E; ++k) y[k] = value_at<DT>(row.p, j + k, j1);
+        *reinterpret_cast<uint4*>(&w[4 * v]) = Type<DT>::vec(y);
       }
-      *reinterpret_cast<uint4*>(&w[4 * v]) = x;
     }
   }
-  __device__ static int64_t column(int64_t j0, int k, int off) {
-    return j0 + ((k / E) * kThreads + static_cast<int>(threadIdx.x)) * E + k % E - off;
+  __device__ static int64_t column(int64_t j0, int k) {
+    return j0 + ((k / E) * kThreads + static_cast<int>(threadIdx.x)) * E + k % E;
   }
   // The lane's maximum, and the sum of e^(lambda (x - F)) (16-bit values are
   // never widened for either).
@@ -309,19 +342,18 @@ struct Tile {
   }
 };
 
-// Best k entries of columns [g0, g1) of the vector grid, exactly, 256 columns
-// at a time (the path of a part whose list overflowed).
+// Best k entries of columns [g0, g1), exactly, 256 columns at a time (the path
+// of a part whose list overflowed).
 template <int DT>
-__device__ __noinline__ void slow_part(List& l, const char* row, int64_t g0, int64_t g1, int off,
-                                       int64_t V, int k) {
+__device__ __noinline__ void slow_part(List& l, const char* row, int64_t g0, int64_t g1, int k) {
   __syncthreads();
   if (threadIdx.x == 0) l.count = 0;
   __syncthreads();
   uint64_t least = 0;  // key of the k-th best once k are known
   bool full = false;
   for (int64_t g = g0; g < g1; g += kThreads) {
-    const int64_t j = g + threadIdx.x - off;
-    const float x = g + threadIdx.x < g1 ? value_at<DT>(row, j, V) : neg_inf();
+    const int64_t j = g + threadIdx.x;
+    const float x = value_at<DT>(row, j, g1);
     const uint64_t key = order_key32(x);
     // columns rise, so an equal value later never replaces an earlier one
     if (x > neg_inf() && (!full || key > least)) push(l, key, static_cast<uint32_t>(j));
@@ -354,19 +386,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
   __syncthreads();
 
   if (live) {
-    const char* row = static_cast<const char*>(a.logits) + r * a.ld * Type<DT>::kBytes;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / Type<DT>::kBytes);
+    Row row;
+    row.begin = static_cast<const char*>(a.logits);
+    row.end = row.begin + ((gridDim.x / a.parts - 1) * a.ld + V) * Type<DT>::kBytes;
+    row.p = row.begin + r * a.ld * Type<DT>::kBytes;
+    row.mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row.p) & 15u);
     const int64_t g0 = (part % a.parts) * a.slice;
-    int64_t g1 = g0 + a.slice;
-    if (g1 > V + off) g1 = V + off;
+    const int64_t g1 = g0 + a.slice < V ? g0 + a.slice : V;
     constexpr int64_t kTile = static_cast<int64_t>(kThreads) * kPer;
     float F = kLowest, S = 0.f, T = neg_inf(), top = neg_inf();  // top: of the lane, so far
     int renew = 0, tile = 0;  // the tile that renews the bound next
     Tile<DT> next;
-    if (g0 < g1) next.load(row, g0, g1, V, off);
+    if (g0 < g1) next.load(row, g0, g1);
     for (int64_t g = g0; g < g1; g += kTile) {
       const Tile<DT> t = next;
-      if (g + kTile < g1) next.load(row, g + kTile, g1, V, off);
+      if (g + kTile < g1) next.load(row, g + kTile, g1);
       const float m = fmaxf(t.max(), neg_inf());  // -inf where all are NaN
       if (m > F + kRaise) {
         S *= ex2((F - m) * kL);
@@ -386,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
           const int at = atomicAdd(&sh.list.count, 1);
           if (at < kList)
             sh.list.idx[at] =
-                static_cast<uint32_t>(Tile<DT>::column(g, __ffs(static_cast<int>(hits)) - 1, off));
+                static_cast<uint32_t>(Tile<DT>::column(g, __ffs(static_cast<int>(hits)) - 1));
         }
       }
     }
@@ -403,10 +437,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
     }
     __syncthreads();
     if (sh.list.count > kList) {
-      slow_part<DT>(sh.list, row, g0, g1, off, V, a.k);
+      slow_part<DT>(sh.list, row.p, g0, g1, a.k);
     } else {
       for (int i = tid; i < sh.list.count; i += kThreads)
-        sh.list.key[i] = order_key32(value_at<DT>(row, sh.list.idx[i], V));
+        sh.list.key[i] = order_key32(value_at<DT>(row.p, sh.list.idx[i], V));
       __syncthreads();
       if (sh.list.count > a.cap) prune(sh.list, a.k);
     }
@@ -747,7 +781,7 @@ cudaError_t launch_reorder_vec(const Reorder& a, unsigned grid, cudaStream_t s) 
 
 }  // namespace
 
-BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count) {
+BeamPlan plan_beam(int64_t rows, int64_t V, int sm_count) {
   // CTAs per row: the number that takes the fewest rounds of CTAs times a
   // CTA's time, in tiles, whose fixed part (the bound, the list, the ticket)
   // is worth about kFixed of them. Measured at 256 rows of 151936 bf16: 8 parts
@@ -756,8 +790,7 @@ BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count) {
   constexpr int64_t tile = static_cast<int64_t>(kThreads) * kPer;
   constexpr int64_t kFixed = 4;
   const int64_t slots = static_cast<int64_t>(sm_count) * kCtasPerSm;
-  // the grid of vectors starts up to `off` columns before a row
-  const int64_t tiles = (V + off + tile - 1) / tile;
+  const int64_t tiles = (V + tile - 1) / tile;
   int64_t most = kBeamSlices / rows;
   most = most < 1 ? 1 : (most < tiles ? most : tiles);
   int64_t best = 1, cost = INT64_MAX;
@@ -777,9 +810,7 @@ BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count) {
 
 cudaError_t launch_beam_select(const BeamSelect& b, int sm_count, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(b.groups) * b.beams;
-  const int eb = elem_bytes(b.dtype);
-  const bool aligned = (reinterpret_cast<uintptr_t>(b.logits) & 15u) == 0 && b.ld * eb % 16 == 0;
-  const BeamPlan p = plan_beam(rows, b.V, aligned ? 0 : 16 / eb - 1, sm_count);
+  const BeamPlan p = plan_beam(rows, b.V, sm_count);
   Select a;
   a.logits = b.logits;
   a.ld = b.ld;

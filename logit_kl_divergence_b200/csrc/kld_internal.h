@@ -250,7 +250,7 @@ struct BeamPlan {
   int parts;      // CTAs per row
   int64_t slice;  // columns of each
 };
-BeamPlan plan_beam(int64_t rows, int64_t V, int off, int sm_count);
+BeamPlan plan_beam(int64_t rows, int64_t V, int sm_count);
 struct BeamSelect {
   const void* logits;
   int64_t ld;

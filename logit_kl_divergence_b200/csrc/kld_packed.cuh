@@ -165,18 +165,20 @@ struct Type<KLD_F16> {
 };
 
 // NW words that start `mis` bytes (0 <= mis < 16) into the NW + 4 words w:
-// a two-stage shift by whole words, then a funnel shift by bytes. With mis a
-// multiple of 4 the last step is the identity.
-template <int NW>
+// a two-stage shift by whole words, then a funnel shift by bytes, which a mis
+// that is a multiple of 4 (kWords) does not need.
+template <int NW, bool kWords = false>
 __device__ __forceinline__ void shift_bytes(uint32_t* w, uint32_t mis) {
   const bool two = (mis & 8u) != 0u, one = (mis & 4u) != 0u;
 #pragma unroll
   for (int i = 0; i < NW + 2; ++i) w[i] = two ? w[i + 2] : w[i];
 #pragma unroll
   for (int i = 0; i < NW + 1; ++i) w[i] = one ? w[i + 1] : w[i];
-  const uint32_t bits = (mis & 3u) * 8u;
+  if constexpr (!kWords) {
+    const uint32_t bits = (mis & 3u) * 8u;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+  }
 }
 
 }  // namespace packed

@@ -419,3 +419,21 @@ def test_finished_beams_at_the_merge_s_list_limit(entries):
         for _ in range(20):
             _check(x, s, k, finished=done, eos=5, beam=beam)
         assert beam.status() == 0
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("v", [3001, 32003, 50257])
+def test_equal_beams_tie_wherever_their_rows_start(dtype, v):
+    """Equal rows that start at different offsets within 16 bytes have equal
+    log-sum-exps, so their entries tie and the lowest beam comes first."""
+    groups, beams = 20, 5
+    x = _rows(groups, v, v).to(DTYPES[dtype])
+    x = x[:, None].expand(groups, beams, v).reshape(groups * beams, v)
+    s = torch.full((groups, beams), -3.0)
+    s[3:] = _scores(groups, 1, 4)[3:].expand(-1, beams)
+    _check(x, s, 10)
+    for shift, ld in ((1, v), (5, v + 2), (0, v + 3)):
+        flat = torch.full((shift + groups * beams * ld,), math.nan, dtype=x.dtype, device=DEV)
+        view = torch.as_strided(flat, x.shape, (ld, 1), shift)
+        view.copy_(x)
+        _check(x, s, 10, logits=view)
