@@ -27,6 +27,7 @@
 // exponential among them, at 55 % of the issue slots. 256 rows of 151936 bf16
 // take 48 us; HBM alone would take 12.
 #include <climits>
+#include <type_traits>
 
 #include "kld_internal.h"
 #include "kld_packed.cuh"
@@ -217,65 +218,21 @@ struct Row {
   const char *begin, *end;
 };
 
-// A tile: each thread NV vectors of E columns, vector v of thread t being the
-// tile's (v * kThreads + t)-th from the row's start on. Rows that start
-// inside a 16-byte vector are read as the two vectors that hold one of
-// theirs, shifted into place: so the columns that a thread sums do not depend
-// on where the row lies, and equal rows have equal sums (on the memory's own
-// grid their log-sum-exps differed by 1e-8, which broke ties between beams).
+// A tile: each thread NV vectors of E columns, a warp's NV * 32 vectors one
+// after another from the row's start on. The columns that a thread sums do not
+// depend on where the row lies, so equal rows have equal sums (on the memory's
+// own grid their log-sum-exps differed by 1e-8, which broke ties between
+// beams).
 template <int DT>
 struct Tile {
   static constexpr int E = 16 / Type<DT>::kBytes;
   static constexpr int NV = kPer / E;
   uint32_t w[4 * NV];
-  // 16 bytes from p on, p mis past a boundary, as they lie in memory.
-  __device__ __forceinline__ static void shifted(const char* p, uint32_t mis, uint32_t* to) {
-    const uint4* a = reinterpret_cast<const uint4*>(p - mis);
-    uint32_t x[8];
-    *reinterpret_cast<uint4*>(x) = __ldg(a);
-    *reinterpret_cast<uint4*>(x + 4) = __ldg(a + 1);
-    packed::shift_bytes<4, DT == KLD_F32>(x, mis);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) to[k] = x[k];
+  // A thread's first vector of the tile; the others follow 32 apart.
+  __device__ __forceinline__ static int first() {
+    return static_cast<int>(threadIdx.x >> 5) * (32 * NV) + static_cast<int>(threadIdx.x & 31);
   }
-  // Columns [j0, j0 + tile) of the row, -inf from j1 on.
-  __device__ void load(const Row& row, int64_t j0, int64_t j1) {
-    constexpr int64_t kCols = static_cast<int64_t>(kThreads) * kPer;
-    constexpr int kVec = kThreads * 16;  // bytes from one vector of a thread to its next
-    const char* tile = row.p + j0 * Type<DT>::kBytes;
-    const char* at = tile + threadIdx.x * 16;
-    if (j0 + kCols <= j1) {  // the whole tile, for all threads
-      if (row.mis == 0) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(reinterpret_cast<const uint4*>(at + v * kVec));
-        return;
-      }
-      if (tile - row.mis >= row.begin && tile + NV * kVec + 16 - row.mis <= row.end) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) shifted(at + v * kVec, row.mis, &w[4 * v]);
-        return;
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t j = j0 + (v * kThreads + static_cast<int>(threadIdx.x)) * E;
-      const char* p = at + v * kVec;
-      if (j + E <= j1 && row.mis == 0) {
-        *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(reinterpret_cast<const uint4*>(p));
-      } else if (j + E <= j1 && p - row.mis >= row.begin && p + 32 - row.mis <= row.end) {
-        shifted(p, row.mis, &w[4 * v]);
-      } else {
-        float y[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) y[k] = value_at<DT>(row.p, j + k, j1);
-        *reinterpret_cast<uint4*>(&w[4 * v]) = Type<DT>::vec(y);
-      }
-    }
-  }
-  __device__ static int64_t column(int64_t j0, int k) {
-    return j0 + ((k / E) * kThreads + static_cast<int>(threadIdx.x)) * E + k % E;
-  }
+  __device__ static int64_t column(int64_t j0, int k) { return j0 + (first() + k / E * 32) * E + k % E; }
   // The lane's maximum, and the sum of e^(lambda (x - F)) (16-bit values are
   // never widened for either).
   __device__ __forceinline__ float max() const {
@@ -342,6 +299,100 @@ struct Tile {
   }
 };
 
+// A tile on its way. Rows that start inside a 16-byte vector (kShift) are
+// loaded as the aligned vectors that hold their first bytes, and shifted when
+// the tile is taken: a lane gets the words it lacks from the next lane, the
+// last one from the warp's next vector. (Loading two vectors for each one and
+// shifting at once, with the wait that this brings: 32x8x151937 bf16 58 us,
+// fp32 66.)
+template <int DT, bool kShift>
+struct Ahead {
+  using T = Tile<DT>;
+  static constexpr int NV = T::NV, E = T::E;
+  uint32_t w[4 * NV + (kShift ? 4 : 0)];
+  bool raw;  // not shifted yet
+
+  // Columns [j0, j0 + tile) of the row, -inf from j1 on.
+  __device__ __forceinline__ void load(const Row& row, int64_t j0, int64_t j1) {
+    constexpr int64_t kCols = static_cast<int64_t>(kThreads) * kPer;
+    const char* tile = row.p + j0 * Type<DT>::kBytes;
+    const char* at = tile + T::first() * 16;
+    raw = false;
+    if (j0 + kCols <= j1) {  // the whole tile, for all threads
+      if constexpr (!kShift) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) vector(at + v * 512, v);
+        return;
+      } else if (tile - row.mis >= row.begin && tile + kThreads * NV * 16 + 16 - row.mis <= row.end) {
+        at -= row.mis;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) vector(at + v * 512, v);
+        if ((threadIdx.x & 31) == 0) vector(at + NV * 512, NV);
+        raw = true;
+        return;
+      }
+    }
+    // A row's last tile, and the matrix's first when it starts inside a vector.
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t j = T::column(j0, v * E);
+      const char* p = at + v * 512;
+      if (j + E <= j1 && !kShift) {
+        vector(p, v);
+      } else if (kShift && j + E <= j1 && p - row.mis >= row.begin && p + 32 - row.mis <= row.end) {
+        uint32_t x[8];
+        *reinterpret_cast<uint4*>(x) = __ldg(reinterpret_cast<const uint4*>(p - row.mis));
+        *reinterpret_cast<uint4*>(x + 4) = __ldg(reinterpret_cast<const uint4*>(p - row.mis) + 1);
+        packed::shift_bytes<4, DT == KLD_F32>(x, row.mis);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * v + k] = x[k];
+      } else {
+        float y[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) y[k] = value_at<DT>(row.p, j + k, j1);
+        *reinterpret_cast<uint4*>(&w[4 * v]) = Type<DT>::vec(y);
+      }
+    }
+  }
+  __device__ __forceinline__ void vector(const char* p, int v) {
+    *reinterpret_cast<uint4*>(&w[4 * v]) = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  // The tile in place (the whole warp together; mis and raw are the CTA's).
+  __device__ __forceinline__ void take(T& t, uint32_t mis) const {
+    if (kShift && raw) {
+      switch (mis >> 2) {
+        case 0: return rotate<0>(t, mis);
+        case 1: return rotate<1>(t, mis);
+        case 2: return rotate<2>(t, mis);
+        default: return rotate<3>(t, mis);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4 * NV; ++k) t.w[k] = w[k];
+  }
+  // Words kWords on, and half a word more where mis has one.
+  template <int kWords>
+  __device__ __forceinline__ void rotate(T& t, uint32_t mis) const {
+    constexpr bool kHalf = DT != KLD_F32;
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const uint32_t bits = (mis & 3u) * 8u;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      uint32_t x[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = w[4 * v + k];
+#pragma unroll
+      for (int k = 0; k < kWords + (kHalf ? 1 : 0); ++k) {
+        const uint32_t give = lane == 0 ? w[kShift ? 4 * (v + 1) + k : 0] : x[k];
+        x[4 + k] = __shfl_sync(0xffffffffu, give, (lane + 1) & 31);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        t.w[4 * v + k] = kHalf ? __funnelshift_r(x[kWords + k], x[kWords + k + 1], bits) : x[kWords + k];
+    }
+  }
+};
+
 // Best k entries of columns [g0, g1), exactly, 256 columns at a time (the path
 // of a part whose list overflowed).
 template <int DT>
@@ -396,34 +447,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
     constexpr int64_t kTile = static_cast<int64_t>(kThreads) * kPer;
     float F = kLowest, S = 0.f, T = neg_inf(), top = neg_inf();  // top: of the lane, so far
     int renew = 0, tile = 0;  // the tile that renews the bound next
-    Tile<DT> next;
-    if (g0 < g1) next.load(row, g0, g1);
-    for (int64_t g = g0; g < g1; g += kTile) {
-      const Tile<DT> t = next;
-      if (g + kTile < g1) next.load(row, g + kTile, g1);
-      const float m = fmaxf(t.max(), neg_inf());  // -inf where all are NaN
-      if (m > F + kRaise) {
-        S *= ex2((F - m) * kL);
-        F = m;
-      }
-      S += t.sum(F);
-      top = fmaxf(top, m);
-      if (tile++ == renew) {
-        // after 1, 2, 4, 8, ... tiles: each time about k more entries pass
-        T = block_bound(top, a.k, min(32, a.k / kWarps + 5), sh.bound);
-        renew = 2 * renew + 1;
-      }
-      if (m >= T && m > neg_inf()) {
-        // Only the columns are noted: taking a value out of 16 registers by
-        // its number costs more than reading the few again at the end.
-        for (unsigned hits = t.at_least(T); hits; hits &= hits - 1u) {
-          const int at = atomicAdd(&sh.list.count, 1);
-          if (at < kList)
-            sh.list.idx[at] =
-                static_cast<uint32_t>(Tile<DT>::column(g, __ffs(static_cast<int>(hits)) - 1));
+    auto pass = [&](auto shift) {
+      Ahead<DT, decltype(shift)::value> next;
+      if (g0 < g1) next.load(row, g0, g1);
+      for (int64_t g = g0; g < g1; g += kTile) {
+        Tile<DT> t;
+        next.take(t, row.mis);
+        if (g + kTile < g1) next.load(row, g + kTile, g1);
+        const float m = fmaxf(t.max(), neg_inf());  // -inf where all are NaN
+        if (m > F + kRaise) {
+          S *= ex2((F - m) * kL);
+          F = m;
+        }
+        S += t.sum(F);
+        top = fmaxf(top, m);
+        if (tile++ == renew) {
+          // after 1, 2, 4, 8, ... tiles: each time about k more entries pass
+          T = block_bound(top, a.k, min(32, a.k / kWarps + 5), sh.bound);
+          renew = 2 * renew + 1;
+        }
+        if (m >= T && m > neg_inf()) {
+          // Only the columns are noted: taking a value out of 16 registers by
+          // its number costs more than reading the few again at the end.
+          for (unsigned hits = t.at_least(T); hits; hits &= hits - 1u) {
+            const int at = atomicAdd(&sh.list.count, 1);
+            if (at < kList)
+              sh.list.idx[at] =
+                  static_cast<uint32_t>(Tile<DT>::column(g, __ffs(static_cast<int>(hits)) - 1));
+          }
         }
       }
-    }
+    };
+    if (row.mis == 0)
+      pass(std::false_type{});
+    else
+      pass(std::true_type{});
     // this CTA's frame and sum
     {
       const float f = warp_max(F);
