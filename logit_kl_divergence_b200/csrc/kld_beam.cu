@@ -62,13 +62,14 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
+// Integers in the order of the values (zeros of either sign are one).
 __device__ __forceinline__ uint64_t order_key(double x) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
+  const uint64_t b = x == 0.0 ? 0ull : static_cast<uint64_t>(__double_as_longlong(x));
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 // The same of an fp32 value, in 32 bits.
 __device__ __forceinline__ uint32_t order_key32(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = x == 0.f ? 0u : __float_as_uint(x);
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float key_value32(uint32_t k) {

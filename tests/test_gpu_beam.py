@@ -437,3 +437,20 @@ def test_equal_beams_tie_wherever_their_rows_start(dtype, v):
         view = torch.as_strided(flat, x.shape, (ld, 1), shift)
         view.copy_(x)
         _check(x, s, 10, logits=view)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_zeros_of_either_sign_tie(dtype):
+    x = torch.zeros((4, 12000))
+    x[:, ::2] = -0.0
+    x[1] = -x[1]
+    x[2, 500:] = -0.0
+    x[3, :700] = -0.0
+    x[3, 700:] = -1.0
+    s = torch.tensor([[0.0, -0.0], [-0.0, 0.0]])
+    for k in (1, 8, 100):
+        _check(x.to(DTYPES[dtype]), s, k)
+    # a single token: its score is the beam's own, zeros of either sign tie too
+    _check(torch.zeros((4, 1), dtype=DTYPES[dtype]), s, 2)
+    done = torch.tensor([[True, False], [False, True]])
+    _check(torch.zeros((4, 1), dtype=DTYPES[dtype]), s, 2, finished=done, eos=0)
