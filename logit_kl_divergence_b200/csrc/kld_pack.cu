@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads)
         h1[i] = kOff ? __ldg(hp + i * (kStep / kBlock) + more) : h0[i];
       }
 #pragma unroll
-      for (int i = 0; i < kUnpackUnits; ++i) special |= h0[i] | h1[i];
+      for (int i = 0; i < kUnpackUnits; ++i) special |= special_bits(h0[i]) | special_bits(h1[i]);
       whole = !(special & 256u);
       if (whole) {
         const int cut = kBlock - static_cast<int>(j0 & (kBlock - 1));  // the first block's columns
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     if (!whole) {
-      // a row's ends, masked or bad blocks
+      // a row's ends, special blocks
 #pragma unroll 1
       for (int i = 0; i < kUnpackUnits; ++i) {
         const int64_t j = j0 + i * kStep;

@@ -36,11 +36,12 @@ constexpr uint32_t kMaskedHead = 256u;
 constexpr uint32_t kBadHead = 0x1ffu;  // base 0, some code is 0, low byte 255
 constexpr float kLimit = 8.507059173023462e37f;  // 2^126
 
-// One block's decoding constants: value = (2^23 + code) * step + off, where
-// off = (base - 2^23) * step is exact (|base - 2^23| < 2^24).
+// One block's decoding constants: value = (2^23 + code + shift) * step, where
+// shift = base - 2^23 (|shift| < 2^24) and the sum are exact.
 struct Scale {
-  float step, off;
+  float step, shift;
   bool masked;  // some code is 0: those entries are -inf
+  __device__ __forceinline__ float value(float magic) const { return (magic + shift) * step; }
 };
 __device__ __forceinline__ Scale scale_of(uint32_t head) {
   Scale s;
@@ -49,13 +50,19 @@ __device__ __forceinline__ Scale scale_of(uint32_t head) {
   // a masked block's (0) is not used.
   const uint32_t field = eb == 255u ? 0x7fc00000u : (eb - 1u) << 23;
   s.step = eb == 0u ? 1.f : __uint_as_float(field);
-  s.off = static_cast<float>((static_cast<int32_t>(head) >> 9) - (1 << 23)) * s.step;
+  s.shift = static_cast<float>((static_cast<int32_t>(head) >> 9) - (1 << 23));
   s.masked = (head & 256u) != 0u && eb != 255u;
   return s;
 }
-// The same for a block without masks or bad values (bit 8 of its header is
-// 0), in a few integer and FMA-pipe operations: the step's bits are the low
-// byte less one in the exponent field; 1.5 * 2^23 + base is made by its bits.
+// A block that is not special has no masks or bad values (bit 8 of its header
+// is 0) and a step below 2^96 (a low byte below 224: adding 32 does not reach
+// bit 8). Bit 8 of this, or of an OR of several, tells.
+__device__ __forceinline__ uint32_t special_bits(uint32_t head) { return head | (head + 32u); }
+// Decoding constants of such a block, value = (2^23 + code) * step + off with
+// off = (base - 2^23) * step exact, in a few integer and FMA-pipe operations:
+// the step's bits are the low byte less one in the exponent field; 1.5 * 2^23 +
+// base is made by its bits. A step past 2^104 can make off, and with it every
+// value, -inf, and does nothing else wrong.
 __device__ __forceinline__ void plain_scale(uint32_t head, float& step, float& off) {
   step = __uint_as_float(head * 0x00800000u - 0x00800000u);
   const float b = __uint_as_float(0x4b400000u + static_cast<uint32_t>(static_cast<int32_t>(head) >> 9));
@@ -71,22 +78,10 @@ __device__ __forceinline__ float magic_byte(uint32_t w) {
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
-// Values of 4 codes of one block.
-__device__ __forceinline__ void decode4(uint32_t w, const Scale& s, float* o) {
-  o[0] = fmaf(magic_byte<0>(w), s.step, s.off);
-  o[1] = fmaf(magic_byte<1>(w), s.step, s.off);
-  o[2] = fmaf(magic_byte<2>(w), s.step, s.off);
-  o[3] = fmaf(magic_byte<3>(w), s.step, s.off);
-  if (s.masked) {
-    if (!(w & 0x000000ffu)) o[0] = neg_inf();
-    if (!(w & 0x0000ff00u)) o[1] = neg_inf();
-    if (!(w & 0x00ff0000u)) o[2] = neg_inf();
-    if (!(w & 0xff000000u)) o[3] = neg_inf();
-  }
-}
+// The value of a code of any block.
 __device__ __forceinline__ float decode1(uint32_t code, uint32_t head) {
   const Scale s = scale_of(head);
-  const float v = fmaf(__uint_as_float(0x4b000000u | code), s.step, s.off);
+  const float v = s.value(__uint_as_float(0x4b000000u | code));
   return s.masked && code == 0u ? neg_inf() : v;
 }
 

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       Heads<QT, kOff> h;
       h.load(slot + Slot<QT>::kHeads, slot + Slot<QT>::kQuant + kCodeBytes, off, lane);
       const uint32_t special = step_plain<QT, kOff>(off, slot, slot + Slot<QT>::kQuant, h, lane, b, q, qw);
-      if (!add_step<QT>(st, b, q, qw, special, 0xffffu, c)) {
+      if (!add_step<QT, true>(st, b, q, qw, special, 0xffffu, c)) {
         if (later < kLater && lane == 0) sh.later[warp].chunk[later] = c;
         ++later;
       }
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   }
   if (!sh.total.good) {  // the same in every thread of the cluster
-    copy_wait<0>();
+    copy_wait<0>();  // (the columns found above may miss what plain_scale could not hold)
     Slow s;
     slow_row<QT>(sh.slow, rp, V, s);
     if (grow) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     __syncthreads();
     if (rank == 0 && tid == 0)
-      write_row(out, sh.tok, r, s.kl, 1.0, s.mb, s.mq, log(s.Sb), log(s.Sq), sh.ib, sh.iq,
+      write_row(out, sh.tok, r, s.kl, 1.0, s.mb, s.mq, log(s.Sb), log(s.Sq), s.ib, s.iq,
                     s.flags);
     return;
   }

@@ -385,6 +385,7 @@ struct Total {
 struct SlowShared {
   double dsum[32];
   float fmax_[2][32];
+  int first[2];  // lowest columns of the maxima
   uint32_t flags;
 };
 
@@ -469,9 +470,11 @@ __device__ __forceinline__ void add_poly(State& s, const float* b, const f2* x) 
 // Adds a chunk's 16 columns of a lane (the whole warp together) to its
 // state. Entries whose bit in `valid` is 0 are -inf in both operands (masks,
 // columns outside the row): they have weight 0 and take x = 0. i: the
-// chunk's number. special: some block of the lane's is (bit 8); then nothing
-// is added and the result is false.
-template <int QT>
+// chunk's number. special: some block of the lane's is masked or bad (bit 8);
+// then nothing is added and the result is false. kPlain: the values come from
+// slot_values, where an entry is -inf only if its block's step is past 2^95
+// (plain_scale); such rows are left to slow_row.
+template <int QT, bool kPlain>
 __device__ __forceinline__ bool add_step(State& s, const float* b, const float* q,
                                          const uint32_t* qw, uint32_t special, unsigned valid, int i) {
   constexpr int kPk = kPacked16<QT>;
@@ -511,7 +514,8 @@ __device__ __forceinline__ bool add_step(State& s, const float* b, const float* 
   } else {
     // Large or non-finite log-ratios. A masked base entry has e = 0 and gives
     // its h to Q; x = -inf with a base entry above -inf makes E non-finite,
-    // which sends the row to slow_row.
+    // which sends the row to slow_row, as a block too wide for plain_scale does.
+    const float none = kPlain ? __int_as_float(0x7fc00000) : 0.f;
     const float G = floorf(warp_max(mq) * kLog2e);
     if (G > s.G) {
       s.Q *= static_cast<float>(pow2d(s.G - G));
@@ -527,7 +531,7 @@ __device__ __forceinline__ bool add_step(State& s, const float* b, const float* 
         const float bk = b[2 * k + h];
         const float e = ex2(fmaf(bk, kLog2e, -s.F));
         D += e;
-        E += bk == neg_inf() ? 0.f : e * xs[h];
+        E += bk == neg_inf() ? none : e * xs[h];
         Q += ex2(fmaf(q_el<kPk>(q, qw, 2 * k + h), kLog2e, -s.G));
       }
     }
@@ -620,7 +624,7 @@ __device__ __noinline__ State add_later(State s, const RowPtr rp, int64_t V, int
   const float mb = s.mb, mq = s.mq;
   const int ib = s.ib, iq = s.iq;
   s.mb = s.mq = neg_inf();
-  add_step<QT>(s, b, q, qw, 0u, valid, c);
+  add_step<QT, false>(s, b, q, qw, 0u, valid, c);
   if (mb > s.mb || (mb == s.mb && ib < c)) {
     s.mb = mb;
     s.ib = ib;
@@ -703,6 +707,7 @@ __device__ __noinline__ void merge(const Part* part, int parts, float scale, Tot
 // row's cluster does it for itself): for rows the fp32 sums cannot hold.
 struct Slow {
   float mb, mq;
+  int ib, iq;
   double Sb, Sq, kl;
   uint32_t flags;
 };
@@ -719,7 +724,10 @@ __device__ double block_sum(SlowShared& sh, double x) {
 template <int QT>
 __device__ __noinline__ void slow_row(SlowShared& sh, const RowPtr& rp, int64_t V, Slow& out) {
   const int tid = static_cast<int>(threadIdx.x);
-  if (tid == 0) sh.flags = 0u;
+  if (tid == 0) {
+    sh.flags = 0u;
+    sh.first[0] = sh.first[1] = INT_MAX;
+  }
   __syncthreads();
   float mb = neg_inf(), mq = neg_inf();
   uint32_t f = 0u;
@@ -749,6 +757,7 @@ __device__ __noinline__ void slow_row(SlowShared& sh, const RowPtr& rp, int64_t 
     f = KLD_ROW_EMPTY;
   double sb = 0.0, sq = 0.0, a = 0.0;
   if (!(f & kExcludedFlags)) {
+    int ib = INT_MAX, iq = INT_MAX;
     for (int64_t j = tid; j < V; j += blockDim.x) {
       const double b = static_cast<double>(base_at<QT>(rp, j)) - mb;
       const double q = static_cast<double>(quant_at<QT>(rp, j)) - mq;
@@ -756,13 +765,19 @@ __device__ __noinline__ void slow_row(SlowShared& sh, const RowPtr& rp, int64_t 
       sb += e;
       sq += exp(q);
       if (b > -INFINITY && q > -INFINITY) a += e * (b - q);
+      if (b == 0.0) ib = min(ib, static_cast<int>(j));
+      if (q == 0.0) iq = min(iq, static_cast<int>(j));
     }
+    if (ib < INT_MAX) atomicMin(&sh.first[0], ib);
+    if (iq < INT_MAX) atomicMin(&sh.first[1], iq);
   }
   sb = block_sum(sh, sb);
   sq = block_sum(sh, sq);
   a = block_sum(sh, a);
   out.mb = mb;
   out.mq = mq;
+  out.ib = sh.first[0];
+  out.iq = sh.first[1];
   out.Sb = sb;
   out.Sq = sq;
   out.kl = (f & KLD_ROW_INF_KL) ? INFINITY : a / sb - log(sb) + log(sq);

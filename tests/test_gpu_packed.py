@@ -505,3 +505,36 @@ def test_gradient_of_quant_rows_that_peak_far_from_the_base_argmax(n, v, peak, g
     tok = torch.full((n,), 9, dtype=torch.int32)
     for scale in (1.0, 1.0 / 2048):
         _check(b, q, tok, "f32" if quant == "packed" else quant, "f32", scale=scale, pack_quant=quant == "packed")
+
+
+def _wide_rows(v):
+    """Rows whose blocks span up to 2^126: steps past 2^95."""
+    b, q, tok = _pair(9, v, 31)
+    for i, m in enumerate((-1e28, -1e30, -6e33, -1e36, -8.5e37)):
+        b[i, 3::5] = m                       # masks that every block holds
+        q[i, 3::5] = m
+    b[5, 7] = -3e37                          # in one block
+    q[5, 7] = -3e37
+    b[6] = -8e37                             # everywhere
+    q[6] = -8e37
+    b[7] = torch.randn(v, generator=torch.Generator().manual_seed(1)).clamp(-2, 2) * 4e37
+    q[7] = b[7]
+    b[8, ::2], b[8, 1::2] = 8e37, -8e37
+    q[8] = b[8]
+    tok[:] = 0
+    return b, q, tok
+
+
+@pytest.mark.parametrize("v", [640, 1003, 9001])
+def test_blocks_of_any_width_read_as_the_format(v):
+    b, q, tok = _wide_rows(v)
+    _check_pack(b)
+    _check_pack(b[:, :512].contiguous())
+    _check_pack(b.bfloat16())
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+@pytest.mark.parametrize("v", [640, 1003, 9001])
+def test_rows_of_wide_blocks(v, quant):
+    b, q, tok = _wide_rows(v)
+    _check(b[:7], q[:7], tok[:7], "f32" if quant == "packed" else quant, "f32", pack_quant=quant == "packed")
