@@ -363,9 +363,8 @@ struct Part {
   float D, E;      // over the others: sums of e, e x
   float G, Q;      // and of 2^(q L - G), G their quant exponentials' frame
   float mb, mq;    // maxima of its columns
-  int tb, tq;      // the first of the warp's chunks that hold them
 };
-constexpr int kPartWords = 13;
+constexpr int kPartWords = 11;
 static_assert(sizeof(Part) == 4 * kPartWords, "Part is stored word by word");
 
 // The row's merged sums and what the gradient pass needs of them.
@@ -568,8 +567,6 @@ __device__ __forceinline__ Part part_of(const State& s) {
   w.Q = sum_lanes(s.Q);
   w.mb = warp_max(s.mb);
   w.mq = warp_max(s.mq);
-  w.tb = __reduce_min_sync(0xffffffffu, s.mb == w.mb ? s.ib : INT_MAX);
-  w.tq = __reduce_min_sync(0xffffffffu, s.mq == w.mq ? s.iq : INT_MAX);
   return w;
 }
 __device__ __forceinline__ State fresh_state() {
