@@ -403,7 +403,13 @@ kld_status_t kld_stats_run_static(const void* base, const void* quant,
  * bits. A block without an entry above -inf has head 256. A block holding
  * NaN, +inf or a magnitude of 2^126 or more has head 511 and reads as NaN:
  * its row is NONFINITE to the statistic. With logits spanning R in a block the
- * error is at most R / 254 either way.
+ * error is at most the larger of R / 254 and 2^-21 max|x| either way; values
+ * that are whole multiples of the step are stored exactly.
+ *
+ * A finite mask (-1e9, a type's lowest value) is an entry like any other: it
+ * spans its block, whose other entries then lie within one step and are lost,
+ * and from 2^126 on it makes the block NaN. Mask with -inf, or let
+ * kld_pack_logits_masked turn such entries into -inf.
  */
 #define KLD_PACK_BLOCK 128
 typedef struct {
@@ -421,6 +427,17 @@ typedef struct {
  */
 kld_status_t kld_pack_logits(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
                              const kld_packed_t* out, int device, void* stream);
+
+/*
+ * kld_pack_logits of logits masked by a finite value: entries at or below
+ * mask_at (rounded to dtype) are stored as -inf and take no part in their
+ * block's step. To the
+ * statistic and the gradient they have no weight, as before (a row of nothing
+ * but masks is EMPTY). KLD_ERR_INVALID_ARG for a mask_at that is NaN or +inf.
+ */
+kld_status_t kld_pack_logits_masked(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+                                    float mask_at, const kld_packed_t* out, int device,
+                                    void* stream);
 
 /*
  * Restore the values of a checkpoint into [N, V] `out` (device, contiguous),

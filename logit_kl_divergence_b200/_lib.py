@@ -157,6 +157,7 @@ SIGNATURES = {
     "kld_stats_timing": (_ST, [_P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     "kld_plan": (_ST, [_I64, _I64, _I32, _I32, ctypes.POINTER(Plan)]),
     "kld_pack_logits": (_ST, [_P, _I64, _I64, _I32, _PK, _I32, _P]),
+    "kld_pack_logits_masked": (_ST, [_P, _I64, _I64, _I32, ctypes.c_float, _PK, _I32, _P]),
     "kld_unpack_logits": (_ST, [_PK, _I64, _I64, _P, _I32, _I32, _P]),
     "kld_stats_run_packed": (_ST, [_P, _PK, _P, _I32, _PK, _P, _I64, _I64, ctypes.POINTER(Fields), _P]),
     "kld_stats_run_grad_packed": (_ST, [_P, _PK, _P, _I32, _PK, _P, _I64, _I64, _P, _I32,

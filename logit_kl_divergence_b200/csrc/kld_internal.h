@@ -211,8 +211,9 @@ cudaError_t launch_topk_threshold(const void* base, int64_t N, int64_t V, kld_dt
                                   int k, float* tf, int sm_count, cudaStream_t stream);
 
 // 8-bit logit checkpoints (format: kld_packed.cuh): codes [N, nb * 128]
-// (16-byte aligned), headers [N, nb], nb = ceil(V / 128).
-cudaError_t launch_pack(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+// (16-byte aligned), headers [N, nb], nb = ceil(V / 128). Entries at or below
+// mask_at (-inf: none but those) are stored as -inf.
+cudaError_t launch_pack(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype, float mask_at,
                         uint8_t* codes, uint32_t* heads, int sm_count, cudaStream_t stream);
 cudaError_t launch_unpack(const uint8_t* codes, const uint32_t* heads, int64_t N, int64_t V,
                           void* out, kld_dtype_t out_dtype, int sm_count, cudaStream_t stream);

@@ -3,6 +3,7 @@
 // and its workspace. The kernels are in kld_pack.cu and kld_beam.cu.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <new>
 
@@ -68,13 +69,20 @@ extern "C" {
 
 kld_status_t kld_pack_logits(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
                              const kld_packed_t* out, int device, void* stream) {
+  return kld_pack_logits_masked(logits, N, V, dtype, -INFINITY, out, device, stream);
+}
+
+kld_status_t kld_pack_logits_masked(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+                                    float mask_at, const kld_packed_t* out, int device,
+                                    void* stream) {
   kld_status_t st = check_matrix(logits, N, V, dtype, out, device);
   if (st != KLD_OK) return st;
+  if (!(mask_at < INFINITY)) return KLD_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = kld::check_device(device, &sms)) != KLD_OK) return st;
   DeviceGuard guard(device);
   if (!guard.ok()) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
-  KLD_CUDA(kld::launch_pack(logits, N, V, dtype, out->codes, out->heads, sms,
+  KLD_CUDA(kld::launch_pack(logits, N, V, dtype, mask_at, out->codes, out->heads, sms,
                             static_cast<cudaStream_t>(stream)));
   return KLD_OK;
 }

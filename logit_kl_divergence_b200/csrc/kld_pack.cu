@@ -1,5 +1,8 @@
 // kld_pack.cu -- writing and restoring the 8-bit logit checkpoint (format
 // and its arithmetic: kld_packed.cuh).
+#include <cmath>
+#include <type_traits>
+
 #include "kld_internal.h"
 #include "kld_packed.cuh"
 
@@ -193,10 +196,10 @@ __device__ __forceinline__ void pack_unit(const float* x, bool live, int lane, u
 // One pass over the logits: a lane holds kPackUnits units of 16 elements in
 // registers and writes each one's codes as one vector. Bound by HBM: it reads
 // s and writes 1 + 1/32 bytes per element; 2048 x 151936 bf16 in 157 us, 6.0
-// TB/s (fp32 244 us, 6.4 TB/s).
-template <int DT, bool kAligned>
+// TB/s (fp32 244 us, 6.4 TB/s). kMask: entries at or below mask_at become -inf.
+template <int DT, bool kAligned, bool kMask>
 __global__ void __launch_bounds__(kThreads)
-    kld_pack_kernel(const void* __restrict__ logits, int64_t N, int64_t V, int64_t nb,
+    kld_pack_kernel(const void* __restrict__ logits, int64_t N, int64_t V, int64_t nb, float mask_at,
                     uint8_t* __restrict__ codes, uint32_t* __restrict__ heads) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t upr = static_cast<uint32_t>(nb * kLanes);  // units per row
@@ -220,6 +223,10 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t u = u0 + 32 * i;
       float x[kUnit];
       Type<DT>::unpack16(raw[i], x);
+      if constexpr (kMask) {
+#pragma unroll
+        for (int k = 0; k < kUnit; ++k) x[k] = x[k] <= mask_at ? neg_inf() : x[k];
+      }
       uint32_t head;
       uint4 c;
       pack_unit(x, u < upr, lane, head, c);
@@ -335,18 +342,18 @@ int blocks_for(int64_t groups, int sm_count) {
   return static_cast<int>(need < most ? need : most);
 }
 
-template <int DT>
-cudaError_t pack_typed(const void* logits, int64_t N, int64_t V, uint8_t* codes, uint32_t* heads,
-                       int sm_count, cudaStream_t s) {
+template <int DT, bool kMask>
+cudaError_t pack_typed(const void* logits, int64_t N, int64_t V, float mask_at, uint8_t* codes,
+                       uint32_t* heads, int sm_count, cudaStream_t s) {
   const int64_t nb = (V + kBlock - 1) / kBlock;
   const bool aligned = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 &&
                        (N == 1 || V * Type<DT>::kBytes % 16 == 0);
   const int64_t group = 32 * (aligned ? kPackUnits<DT, true> : kPackUnits<DT, false>);
   const int grid = blocks_for(N * ((nb * kLanes + group - 1) / group), sm_count);
   if (aligned)
-    kld_pack_kernel<DT, true><<<grid, kThreads, 0, s>>>(logits, N, V, nb, codes, heads);
+    kld_pack_kernel<DT, true, kMask><<<grid, kThreads, 0, s>>>(logits, N, V, nb, mask_at, codes, heads);
   else
-    kld_pack_kernel<DT, false><<<grid, kThreads, 0, s>>>(logits, N, V, nb, codes, heads);
+    kld_pack_kernel<DT, false, kMask><<<grid, kThreads, 0, s>>>(logits, N, V, nb, mask_at, codes, heads);
   return cudaGetLastError();
 }
 
@@ -367,12 +374,21 @@ cudaError_t unpack_typed(const uint8_t* codes, const uint32_t* heads, int64_t N,
 
 }  // namespace
 
-cudaError_t launch_pack(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype,
+cudaError_t launch_pack(const void* logits, int64_t N, int64_t V, kld_dtype_t dtype, float mask_at,
                         uint8_t* codes, uint32_t* heads, int sm_count, cudaStream_t stream) {
+  auto typed = [&](auto kind) {
+    constexpr int DT = decltype(kind)::value;
+    // as the logits hold it: -1e9 in bf16 is a little above -1e9
+    if (DT == KLD_BF16) mask_at = __bfloat162float(__float2bfloat16_rn(mask_at));
+    if (DT == KLD_F16) mask_at = __half2float(__float2half_rn(mask_at));
+    return mask_at > -INFINITY
+               ? pack_typed<DT, true>(logits, N, V, mask_at, codes, heads, sm_count, stream)
+               : pack_typed<DT, false>(logits, N, V, mask_at, codes, heads, sm_count, stream);
+  };
   switch (dtype) {
-    case KLD_F32: return pack_typed<KLD_F32>(logits, N, V, codes, heads, sm_count, stream);
-    case KLD_BF16: return pack_typed<KLD_BF16>(logits, N, V, codes, heads, sm_count, stream);
-    case KLD_F16: return pack_typed<KLD_F16>(logits, N, V, codes, heads, sm_count, stream);
+    case KLD_F32: return typed(std::integral_constant<int, KLD_F32>{});
+    case KLD_BF16: return typed(std::integral_constant<int, KLD_BF16>{});
+    case KLD_F16: return typed(std::integral_constant<int, KLD_F16>{});
   }
   return cudaErrorInvalidValue;
 }

@@ -124,10 +124,18 @@ class PackedLogits:
         return out
 
 
-def pack_logits(logits: torch.Tensor, out: PackedLogits | None = None, stream=None) -> PackedLogits:
+def pack_logits(logits: torch.Tensor, out: PackedLogits | None = None, stream=None,
+                mask_at: float | None = None) -> PackedLogits:
     """The 8-bit checkpoint of contiguous [N, V] CUDA logits (float32,
     bfloat16 or float16), written to ``out`` (for instance ``store.rows(a, b)``)
-    or to a new one. Asynchronous on the stream."""
+    or to a new one. Asynchronous on the stream.
+
+    Every block of 128 columns has one step, about 1/254 of what its entries
+    span (-inf apart). So logits masked with a finite value need ``mask_at``:
+    entries at or below it (as the logits' type holds it) are stored as -inf.
+    Without it a mask of -1e9 leaves nothing of its block's other entries, and
+    one of 2^126 or more in magnitude (``torch.finfo(dtype).min`` of float32
+    and bfloat16) makes the row NONFINITE to the statistic."""
     lib = _lib.load()
     if logits.dtype not in _DTYPES:
         raise TypeError(f"unsupported logit dtype {logits.dtype}")
@@ -143,8 +151,12 @@ def pack_logits(logits: torch.Tensor, out: PackedLogits | None = None, stream=No
             _empty(stream, (n, blocks), torch.int32, logits.device), logits.shape[1])
     elif out.shape != tuple(logits.shape) or out.device != logits.device:
         raise ValueError("out must hold as many rows and columns on the logits' device")
-    if len(out):
+    if len(out) and mask_at is None:
         _lib.check(lib.kld_pack_logits(logits.data_ptr(), logits.shape[0], logits.shape[1],
                                        _DTYPES[logits.dtype], ctypes.byref(out._c), logits.device.index, s),
                    "kld_pack_logits")
+    elif len(out):
+        _lib.check(lib.kld_pack_logits_masked(logits.data_ptr(), logits.shape[0], logits.shape[1],
+                                              _DTYPES[logits.dtype], float(mask_at), ctypes.byref(out._c),
+                                              logits.device.index, s), "kld_pack_logits_masked")
     return out

@@ -538,3 +538,66 @@ def test_blocks_of_any_width_read_as_the_format(v):
 def test_rows_of_wide_blocks(v, quant):
     b, q, tok = _wide_rows(v)
     _check(b[:7], q[:7], tok[:7], "f32" if quant == "packed" else quant, "f32", pack_quant=quant == "packed")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("v", [1000, 4099])
+def test_finite_masks_are_stored_as_none(dtype, v):
+    """Rows masked by the type's lowest value or another finite one: with
+    mask_at the checkpoint of the same rows masked by -inf."""
+    dt = DTYPES[dtype]
+    b = _pair(6, v, v)[0].to(dt)
+    mask = torch.rand((6, v), generator=torch.Generator().manual_seed(2)) < 0.3
+    mask[4], mask[5] = True, False
+    mask[3, 128:256] = True
+    none = b.masked_fill(mask, -math.inf)
+    want = pack_logits(none.to(DEV))
+    for mask_at in (torch.finfo(dt).min, -1e4, -60000.1) + ((-1e9,) if dtype != "f16" else ()):
+        m = torch.tensor(mask_at, dtype=dt)
+        x = b.masked_fill(mask, m.item())
+        got = pack_logits(x.to(DEV), mask_at=mask_at)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.heads, want.heads)
+        x[0, ::7] = -math.inf                        # masks of both kinds
+        got, same = pack_logits(x.to(DEV), mask_at=mask_at), pack_logits(x.masked_fill(x <= m, -math.inf).to(DEV))
+        assert torch.equal(got.codes, same.codes) and torch.equal(got.heads, same.heads)
+    # NaN and +inf are not masks
+    x = b.clone()
+    x[1, 5], x[2, 7] = math.nan, math.inf
+    got, same = pack_logits(x.to(DEV), mask_at=-1e4), pack_logits(x.to(DEV))
+    assert torch.equal(got.codes, same.codes) and torch.equal(got.heads, same.heads)
+    with pytest.raises(KLDError):
+        pack_logits(b.to(DEV), mask_at=math.nan)
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16"])
+def test_rows_masked_by_the_type_s_lowest_value(quant):
+    """KL and gradient of base rows masked by finfo.min, stored with mask_at,
+    against those of the dense rows: the masked entries have no weight either
+    way. A stored value is off by at most d = R / 254, R the row's span, so ln p
+    by 2d and p by a factor within e^(+-2d); KL changes by sum p' (ln p' - ln p)
+    + sum (p' - p) ln(p / r)."""
+    dt = DTYPES[quant]
+    n, v = 5, 3001
+    b, q, tok = _pair(n, v, 8)
+    low = torch.finfo(dt).min
+    b[:, 7::3], q[:, 7::3] = low, low
+    b, q, tok = b.to(dt), q.to(dt), torch.full((n,), 1, dtype=torch.int32)
+    keep = (b > low).numpy()
+    base = pack_logits(b.to(DEV), mask_at=low)
+    with KLDStats(n, DEV) as st:
+        g, rows = st.run_grad_packed(base, q.to(DEV), tok.to(DEV), grad_dtype=torch.float32, per_row=True)
+        assert st.result()["n_valid"] == n
+    x, y = b.double().numpy(), q.double().numpy()
+    span = np.where(keep, x, np.nan)
+    d = (np.nanmax(span) - np.nanmin(span)) / 254
+    for i in range(n):
+        lp = np.where(keep[i], x[i], -np.inf)
+        lp = lp - np.logaddexp.reduce(lp)
+        lr = np.where(keep[i], y[i], -np.inf)
+        lr = lr - np.logaddexp.reduce(lr)
+        p, r = np.exp(lp), np.exp(lr)
+        gap = np.where(keep[i], np.abs(np.where(keep[i], lp, 0.0) - np.where(keep[i], lr, 0.0)), 0.0)
+        kl = (p * np.where(keep[i], np.where(keep[i], lp, 0.0) - np.where(keep[i], lr, 0.0), 0.0)).sum()
+        assert abs(rows["kld"][i].item() - kl) <= 2 * d + math.expm1(2 * d) * (p * gap).sum() + 1e-6 + 1e-4 * kl
+        off = np.abs(g[i].cpu().double().numpy() - (r - p))
+        assert (off <= p * math.expm1(2 * d) + 4e-6 * (p + r) + 1e-12).all()

@@ -145,3 +145,13 @@ def test_states_that_share_memory_are_told_from_those_that_interleave():
     flat = torch.zeros(64)
     assert not pair(flat[:60].view(6, 10), flat[4:64].view(12, 5)[:6])
     assert pair(flat[:30].view(6, 5), flat[30:60].view(6, 5))
+
+
+def test_masked_pack_refuses(lib):
+    x = ctypes.c_void_p(P)
+    f = lambda m, dt=0, pk=_pk(4 * P, 8 * P): lib.kld_pack_logits_masked(x, 4, 8, dt, m, pk, 1 << 20, None)
+    assert f(float("nan")) == INVALID and f(float("inf")) == INVALID
+    assert f(-1e9, dt=3) == DTYPE and f(-1e9, pk=None) == INVALID and f(-1e9, pk=_pk()) == INVALID
+    if not torch.cuda.is_available():
+        for m in (-1e9, 0.0, float("-inf")):
+            assert f(m) == _lib.KLD_ERR_NO_DEVICE
