@@ -102,6 +102,18 @@ def _describe(t: torch.Tensor, time_dim: int | None) -> _lib.State:
                       0 if time_dim is None else 1, 0)
 
 
+def _holds(s: _lib.State, rows: int, a: int, b: int) -> bool:
+    """Whether a state's runs hold any of the bytes [a, b), counted from its
+    first one."""
+    run = s.positions * s.position_bytes
+    for r in range(rows if s.row_stride else 1):
+        first = a - run - r * s.row_stride + 1  # the lowest start of a run that reaches a
+        i = max(0, -(-first // s.outer_stride)) if s.outer > 1 else (0 if first <= 0 else 1)
+        if i < s.outer and r * s.row_stride + i * s.outer_stride < b:
+            return True
+    return False
+
+
 class BeamStates:
     """States that :meth:`BeamSearch.reorder` moves together, described once
     (it holds the tensors, whose memory must stay where it is)."""
@@ -116,7 +128,7 @@ class BeamStates:
         if any(t.device != device for t in self.tensors):
             raise ValueError("states must be on the handle's device")
         self.spans = [_span(t) for t in self.tensors]
-        layouts = [_describe(t, d) for t, d in items]
+        self.layouts = layouts = [_describe(t, d) for t, d in items]
         order = sorted(((span, layout, self.rows) for span, layout in zip(self.spans, layouts)
                         if span[0] < span[1]), key=lambda a: a[0])
         for i, a in enumerate(order):
@@ -129,6 +141,13 @@ class BeamStates:
 
     def __len__(self) -> int:
         return len(self.tensors)
+
+    def hold(self, t: torch.Tensor) -> bool:
+        """Whether a contiguous tensor shares memory with a state (the gaps
+        between a state's runs are not its own)."""
+        a, b = _span(t)
+        return any(a < y and x < b and _holds(s, self.rows, a - x, b - x)
+                   for (x, y), s in zip(self.spans, self.layouts))
 
 
 class BeamSearch:
@@ -246,8 +265,7 @@ class BeamSearch:
                 continue
             if t.device != self.device:
                 raise ValueError("parents and lengths must be on the handle's device")
-            a, b = _span(t)
-            if any(a < y and x < b for x, y in states.spans):
+            if states.hold(t):
                 raise ValueError("parents and lengths may not lie in a state")
         _lib.check(self._lib.kld_beam_reorder(self._h, states._c, len(states.tensors), parents.data_ptr(),
                                               _ptr(lengths), parents.shape[0], parents.shape[1],

@@ -454,3 +454,24 @@ def test_zeros_of_either_sign_tie(dtype):
     _check(torch.zeros((4, 1), dtype=DTYPES[dtype]), s, 2)
     done = torch.tensor([[True, False], [False, True]])
     _check(torch.zeros((4, 1), dtype=DTYPES[dtype]), s, 2, finished=done, eos=0)
+
+
+def test_parents_and_lengths_between_the_rows_of_a_state():
+    """A state seen as part of wider rows, its parents and lengths kept in the
+    rows' ends."""
+    groups, beams = 2, 3
+    wide = torch.arange(6 * 20, dtype=torch.int32).view(6, 20).to(DEV)
+    p = torch.tensor([[1, 0, 0], [2, 2, 1]], dtype=torch.int32)
+    lengths = torch.tensor([12, 3, 0, 5, 11, 7], dtype=torch.int32)
+    parents, lens = wide[2, 14:20].view(groups, beams), wide[4, 13:19]
+    parents.copy_(p), lens.copy_(lengths)
+    before = wide.cpu().numpy()
+    want = before.copy()
+    want[:, :12] = packed_ref.reorder(before[:, :12], p.numpy(), lengths.numpy(), 1)
+    with BeamSearch(groups, beams, device=DEV) as beam:
+        beam.reorder([(wide[:, :12], 1)], parents, lens)
+        assert np.array_equal(wide.cpu().numpy(), want)
+        with pytest.raises(ValueError):
+            beam.reorder([(wide[:, :15], 1)], parents, lens)
+        with pytest.raises(ValueError):
+            beam.reorder([(wide[:, :14], 1)], parents, lens)

@@ -155,3 +155,27 @@ def test_masked_pack_refuses(lib):
     if not torch.cuda.is_available():
         for m in (-1e9, 0.0, float("-inf")):
             assert f(m) == _lib.KLD_ERR_NO_DEVICE
+
+
+def test_what_a_state_holds_is_told_from_the_gaps_in_it():
+    """parents and lengths may lie between a state's rows or runs."""
+    buf = torch.zeros((4, 3, 6, 10))                 # rows, heads, time, dim
+    state = buf[:, :, :4]                            # two positions of every run are free
+
+    def held(t, where):
+        s = BeamStates.__new__(BeamStates)
+        s.tensors, s.rows = [_Cuda(t)], t.shape[0]
+        s.spans, s.layouts = [_span(t)], [_describe(_Cuda(t), 2 if t.dim() == 4 else None)]
+        return s.hold(where)
+
+    for r in range(4):
+        for h in range(3):
+            run = buf[r, h].view(-1)
+            assert not held(state, run[40:60]) and held(state, run[39:60])
+            assert held(state, run[:1]) and held(state, run[20:24])
+            assert not held(buf[:, :2], run[:]) if h == 2 else held(buf[:, :2], run[:1])
+            assert held(state, buf.view(-1)[(r * 3 + h) * 60 + 59 - (59 if (r, h) == (3, 2) else 0):][:2])
+    assert not held(buf[1:3].view(2, -1), buf[3, 0, 0, :4]) and not held(buf[1:3].view(2, -1), buf[0, 2, 5, 6:])
+    assert held(buf[1:3].view(2, -1), buf[2, 2, 5, 6:])
+    one = buf[:1, :1]                                # one row, one run
+    assert not held(one, buf[0, 1, 0]) and held(one, buf[0, 0, 5, 9:])
