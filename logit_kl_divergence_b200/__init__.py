@@ -179,7 +179,10 @@ class KLDStats:
                    per_row: bool = False, stream=None) -> dict | None:
         """:meth:`run` with the base rows read from an 8-bit checkpoint; the
         quant rows are a dense [N, V] tensor (any of the three dtypes) or a
-        checkpoint too. The statistic is that of the stored values. With
+        checkpoint too. The statistic is that of the stored values: of logits
+        of standard deviation 2.5 these are about 2.3e-4 nats from the rows
+        themselves, so a KL of 1e-3 is off by a fifth, one of 0.06 by under
+        1 %. With
         ``per_row``, returns ``kld`` and ``nll`` (float64), ``amax_b`` and
         ``amax_q`` (int32) as CUDA tensors of N values. Asynchronous on the
         stream."""
@@ -192,8 +195,11 @@ class KLDStats:
                         per_row: bool = False, stream=None):
         """:meth:`run_packed` plus the gradient with respect to the quant
         logits, as :meth:`run_grad` gives it (``grad_dtype``: the quant
-        logits' by default, float32 for packed ones), in one kernel; ``out`` may be the dense quant tensor itself. Returns the gradient, or (gradient, rows) with ``per_row``.
-        Asynchronous on the stream."""
+        logits' by default, float32 for packed ones), in one kernel; ``out``
+        may be the dense quant tensor itself. Returns the gradient, or
+        (gradient, rows) with ``per_row``. Where KL is near 1e-3 the storage's
+        rounding is most of the gradient (:meth:`run_packed`). Asynchronous on
+        the stream."""
         head, fields, rows, s = self._packed_call(base, quant, token_ids, per_row, stream)
         if out is None:
             dt = grad_dtype or (torch.float32 if isinstance(quant, PackedLogits) else quant.dtype)

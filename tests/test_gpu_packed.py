@@ -601,3 +601,38 @@ def test_rows_masked_by_the_type_s_lowest_value(quant):
         assert abs(rows["kld"][i].item() - kl) <= 2 * d + math.expm1(2 * d) * (p * gap).sum() + 1e-6 + 1e-4 * kl
         off = np.abs(g[i].cpu().double().numpy() - (r - p))
         assert (off <= p * math.expm1(2 * d) + 4e-6 * (p + r) + 1e-12).all()
+
+
+@pytest.mark.parametrize("quant", ["f32", "packed"])
+@pytest.mark.parametrize("noise", [0.05, 0.4])
+def test_what_eight_bits_change(noise, quant):
+    """KL and gradient from checkpoints against those of the logits that were
+    stored. A stored value is off by at most d = max(R / 254, 2^-21 max|x|) in
+    a block that spans R, so with d the row's largest (e for quant rows, 0 when
+    dense) ln p moves by 2d, p by a factor within e^(+-2d), and
+    KL by |sum p' ((ln p' - ln p) - (ln r' - ln r)) + sum (p' - p) ln(p / r)|
+    <= 2d + 2e + (e^(2d) - 1) sum p |ln(p / r)|."""
+    n, v = 8, 5003
+    g = torch.Generator().manual_seed(17)
+    b, _, tok = _pair(n, v, 17)
+    q = b + noise * torch.randn((n, v), generator=g)
+
+    def off(x):
+        t = torch.nn.functional.pad(x, (0, -v % 128), value=math.nan).view(n, -1, 128).numpy()
+        span = np.nanmax(t, 2) - np.nanmin(t, 2)
+        return np.maximum(span / 254, 2.0 ** -21 * np.nanmax(np.abs(t), 2)).max(1).astype(np.float64)
+
+    base = pack_logits(b.to(DEV))
+    other = pack_logits(q.to(DEV)) if quant == "packed" else q.to(DEV)
+    d, e = off(b), off(q) if quant == "packed" else np.zeros(n)
+    stored = np.abs(_np(base.unpack()).astype(np.float64) - b.numpy())
+    assert (stored.max(1) <= d).all()
+    with KLDStats(n, DEV) as st:
+        grad, rows = st.run_grad_packed(base, other, tok.to(DEV), grad_dtype=torch.float32, per_row=True)
+    kld, grad = rows["kld"].cpu().numpy(), grad.cpu().double().numpy()
+    p, r = packed_ref.softmax(b.numpy()), packed_ref.softmax(q.numpy())
+    ratio = np.log(p) - np.log(r)
+    kl = (p * ratio).sum(1)
+    assert (np.abs(kld - kl) <= 2 * d + 2 * e + np.expm1(2 * d) * (p * np.abs(ratio)).sum(1) + 1e-6 + 1e-4 * kl).all()
+    far = p * np.expm1(2 * d)[:, None] + r * np.expm1(2 * e)[:, None] + 4e-6 * (p + r) * np.exp(2 * (d + e))[:, None]
+    assert (np.abs(grad - (r - p)) <= far + 1e-12).all()
