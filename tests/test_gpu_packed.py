@@ -636,3 +636,30 @@ def test_what_eight_bits_change(noise, quant):
     assert (np.abs(kld - kl) <= 2 * d + 2 * e + np.expm1(2 * d) * (p * np.abs(ratio)).sum(1) + 1e-6 + 1e-4 * kl).all()
     far = p * np.expm1(2 * d)[:, None] + r * np.expm1(2 * e)[:, None] + 4e-6 * (p + r) * np.exp(2 * (d + e))[:, None]
     assert (np.abs(grad - (r - p)) <= far + 1e-12).all()
+
+
+@pytest.mark.parametrize("quant", ["f32", "bf16", "packed"])
+def test_long_rows_of_random_logits(quant):
+    """2^22 + 77 and 2^25 + 1 columns a row, taken by one CTA or a cluster:
+    a lane adds 10^3 to 10^5 terms, whose sums keep the tolerances."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    for n, v in ((1, (1 << 25) + 1), (6, (1 << 22) + 77), (400, (1 << 20) + 3)):
+        b = torch.randn((n, v), generator=g, device=DEV) * 2.0
+        q = b + torch.randn((n, v), generator=g, device=DEV) * 0.3
+        q = q.to(DTYPES["f32" if quant == "packed" else quant])
+        base = pack_logits(b)
+        other = pack_logits(q) if quant == "packed" else q
+        del b
+        tok = torch.randint(0, v, (n,), generator=g, device=DEV, dtype=torch.int32)
+        with KLDStats(n, device=DEV) as st:
+            grad, rows = st.run_grad_packed(base, other, tok, scale=1.0, grad_dtype=torch.float32, per_row=True)
+        for i in range(0, n, 57):
+            lp = torch.log_softmax(base.rows(i, i + 1).unpack()[0].double(), 0)
+            lr = torch.log_softmax((other.rows(i, i + 1).unpack()[0] if quant == "packed" else q[i]).double(), 0)
+            p, r = lp.exp(), lr.exp()
+            kl, nll = (p * (lp - lr)).sum().item(), -lr[tok[i].long()].item()
+            assert abs(rows["kld"][i].item() - kl) <= 1e-6 + 1e-4 * kl, (v, rows["kld"][i].item(), kl)
+            assert abs(rows["nll"][i].item() - nll) <= 1e-6 + 1e-4 * nll
+            off = ((grad[i].double() - (r - p)).abs() - 1e-12) / (p + r)
+            assert off.max().item() <= 4e-6, (v, i, off.max().item())
+        del grad, q, base, other
