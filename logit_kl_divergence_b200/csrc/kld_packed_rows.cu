@@ -134,29 +134,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   }
   int cur = 0, nxt = kDepth == slots ? 0 : kDepth;  // slots of chunks i and i + kDepth
-  for (int i = 0; i < n; ++i) {
-    copy_wait<kDepth - 1>();
-    __syncwarp();
-    int c = first + i * (kSub * kWarps);
-    const int end = c + kSub < d1 ? c + kSub : d1;
-    uint32_t slot = my + cur * kPair;
-#pragma unroll 1
-    for (; c < end; ++c, slot += Slot<QT>::kBytes) {
-      float b[16], q[16];
-      uint32_t qw[8];
-      Heads<QT, kOff> h;
-      h.load(slot + Slot<QT>::kHeads, slot + Slot<QT>::kQuant + kCodeBytes, off, lane);
-      const uint32_t special = step_plain<QT, kOff>(off, slot, slot + Slot<QT>::kQuant, h, lane, b, q, qw);
-      if (!add_step<QT, true>(st, b, q, qw, special, 0xffffu, c)) {
-        if (later < kLater && lane == 0) sh.later[warp].chunk[later] = c;
-        ++later;
-      }
+  Long moved;  // sums of the chunks before the last kFold
+  bool folded = false;
+  for (int stop = 0, i = 0; i < n;) {
+    if (i > 0) {
+      st = fold(st, &moved, !folded);
+      folded = true;
     }
-    __syncwarp();
-    if (i + kDepth < n) load(i + kDepth, nxt);
-    copy_commit();
-    if (++cur == slots) cur = 0;
-    if (++nxt == slots) nxt = 0;
+    stop = stop + kFold / kSub < n ? stop + kFold / kSub : n;
+    for (; i < stop; ++i) {
+      copy_wait<kDepth - 1>();
+      __syncwarp();
+      int c = first + i * (kSub * kWarps);
+      const int end = c + kSub < d1 ? c + kSub : d1;
+      uint32_t slot = my + cur * kPair;
+#pragma unroll 1
+      for (; c < end; ++c, slot += Slot<QT>::kBytes) {
+        float b[16], q[16];
+        uint32_t qw[8];
+        Heads<QT, kOff> h;
+        h.load(slot + Slot<QT>::kHeads, slot + Slot<QT>::kQuant + kCodeBytes, off, lane);
+        const uint32_t special = step_plain<QT, kOff>(off, slot, slot + Slot<QT>::kQuant, h, lane, b, q, qw);
+        if (!add_step<QT, true>(st, b, q, qw, special, 0xffffu, c)) {
+          if (later < kLater && lane == 0) sh.later[warp].chunk[later] = c;
+          ++later;
+        }
+      }
+      __syncwarp();
+      if (i + kDepth < n) load(i + kDepth, nxt);
+      copy_commit();
+      if (++cur == slots) cur = 0;
+      if (++nxt == slots) nxt = 0;
+    }
   }
 
   // The chunks put off, `one` for each; falls: the pairs passed falling.
@@ -179,7 +188,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     later = 0;
     __syncwarp();
   };
-  if (later > 0) others(false, [&](int c) { st = add_later<QT>(st, rp, V, c, lane); });
+  if (later > 0) {
+    int since = 0;
+    others(false, [&](int c) {
+      if (++since == kFold) {
+        st = fold(st, &moved, !folded);
+        folded = true;
+        since = 0;
+      }
+      st = add_later<QT>(st, rp, V, c, lane);
+    });
+  }
   if (edge >= 0 && edge == edge1) {
     if (sh.edge[0][lane] > st.mb) {
       st.mb = sh.edge[0][lane];
@@ -193,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // ---- merge: lanes, then every warp of the cluster
   {
-    const Part w = part_of(st);
+    if (folded) st = fold(st, &moved, false);
+    const Part w = folded ? part_of_long(st, &moved) : part_of(st);
     if (C > 1) cluster_wait();  // every CTA of the cluster has started
     if (lane < C) {             // lane k leaves the part with CTA k
       const uint32_t* words = reinterpret_cast<const uint32_t*>(&w);

@@ -20,8 +20,10 @@
 // rows that are nearly equal or nearly one-hot keep their accuracy, and so do
 // rows whose two distributions hardly meet. F and K belong to a
 // warp and move only when a value exceeds the maximum they were set at by
-// more than four nats. Sums run in fp32 over a lane's part of the row (a few
-// hundred terms) and its warp, in fp64 from there on.
+// more than four nats. Sums run in fp32 over a lane's 16 columns of a chunk,
+// from there over at most kFold chunks and the warp, in fp64 beyond. (Equal
+// terms round alike, so their errors add up: in sums of one fp32 addition a
+// term, gradients of rows of one value were off by 3e-5 over 2^20 columns.)
 //
 // Rows whose sums are not finite and positive (NaN or +inf, an empty row, a
 // base entry above -inf where quant is -inf, magnitudes near the type's
@@ -454,16 +456,20 @@ __device__ __forceinline__ void raise(State& s, const float* b, const float* q, 
 template <int T>
 __device__ __forceinline__ void add_poly(State& s, const float* b, const f2* x) {
   const f2 L2 = splat(kLog2e), nf = splat(-s.F);
+  f2 S, A, C;  // of the step: one addition to the long sums a step
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     float u0, u1;
     upk(fma2(pk(b[2 * k], b[2 * k + 1]), L2, nf), u0, u1);
     const f2 e = pk(ex2(u0), ex2(u1));
     const f2 t = mul2(e, x[k]);
-    s.S = add2(s.S, e);
-    s.A = add2(s.A, t);
-    s.C = fma2(mul2(t, x[k]), phi_q2<T>(x[k]), s.C);
+    S = k == 0 ? e : add2(S, e);
+    A = k == 0 ? t : add2(A, t);
+    C = k == 0 ? mul2(mul2(t, x[k]), phi_q2<T>(x[k])) : fma2(mul2(t, x[k]), phi_q2<T>(x[k]), C);
   }
+  s.S = add2(s.S, S);
+  s.A = add2(s.A, A);
+  s.C = add2(s.C, C);
 }
 
 // Adds a chunk's 16 columns of a lane (the whole warp together) to its
@@ -565,6 +571,69 @@ __device__ __forceinline__ Part part_of(const State& s) {
   w.E = sum_lanes(s.E);
   w.G = s.G;
   w.Q = sum_lanes(s.Q);
+  w.mb = warp_max(s.mb);
+  w.mq = warp_max(s.mq);
+  return w;
+}
+
+// A lane's sums over blocks of kFold chunks, for rows that have more.
+constexpr int kFold = 256;
+struct Long {
+  float F, K, G;
+  double S, A, C, D, E, Q;
+};
+// Moves a lane's sums there (`first`: nothing is there yet), rebasing what is
+// as raise does.
+__device__ __noinline__ State fold(State s, Long* l, bool first) {
+  if (first) {
+    l->F = l->G = kNoFrame;
+    l->K = 0.f;
+    l->S = l->A = l->C = l->D = l->E = l->Q = 0.0;
+  }
+  if (s.F != l->F || s.K != l->K) {
+    const double sc = pow2d(l->F - s.F);
+    const double d = static_cast<double>(s.K) - static_cast<double>(l->K);
+    const double e1 = expm1(kLambda * d), phi = e1 - kLambda * d;
+    if (l->F != kNoFrame) {
+      l->C = sc * (l->C + e1 * l->C + e1 * kLambda * l->A + phi * l->S);
+      l->A = sc * (l->A + d * l->S);
+      l->E = sc * (l->E + d * l->D);
+      l->S *= sc;
+      l->D *= sc;
+    }
+    l->F = s.F;
+    l->K = s.K;
+  }
+  if (s.G > l->G) {
+    l->Q *= pow2d(l->G - s.G);
+    l->G = s.G;
+  }
+  float v0, v1;
+  upk(s.S, v0, v1);
+  l->S += static_cast<double>(v0) + v1;
+  upk(s.A, v0, v1);
+  l->A += static_cast<double>(v0) + v1;
+  upk(s.C, v0, v1);
+  l->C += static_cast<double>(v0) + v1;
+  l->D += s.D;
+  l->E += s.E;
+  l->Q += s.Q;
+  s.S = s.A = s.C = splat(0.f);
+  s.D = s.E = s.Q = 0.f;
+  return s;
+}
+// A warp's part from what was moved (the whole warp together).
+__device__ __noinline__ Part part_of_long(const State s, const Long* l) {
+  Part w;
+  w.F = l->F;
+  w.K = l->K;
+  w.S = static_cast<float>(warp_sum(l->S));
+  w.A = static_cast<float>(warp_sum(l->A));
+  w.C = static_cast<float>(warp_sum(l->C));
+  w.D = static_cast<float>(warp_sum(l->D));
+  w.E = static_cast<float>(warp_sum(l->E));
+  w.G = l->G;
+  w.Q = static_cast<float>(warp_sum(l->Q));
   w.mb = warp_max(s.mb);
   w.mq = warp_max(s.mq);
   return w;

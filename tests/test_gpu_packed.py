@@ -663,3 +663,27 @@ def test_long_rows_of_random_logits(quant):
             off = ((grad[i].double() - (r - p)).abs() - 1e-12) / (p + r)
             assert off.max().item() <= 4e-6, (v, i, off.max().item())
         del grad, q, base, other
+
+
+@pytest.mark.parametrize("value", [0.1, 0.3, 0.45, 5.3])
+@pytest.mark.parametrize("n,v", [(400, 151936), (400, 1 << 20), (1, 1 << 22), (1, 1 << 25)])
+def test_long_rows_of_equal_values(n, v, value):
+    """Equal terms round alike, so that the errors of a long fp32 sum add up."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for step in (0.0, 0.7):
+        b = torch.full((n, v), value, device=DEV)
+        b[:, ::2] -= step
+        base = pack_logits(b)
+        q = b.fill_(value).add_(0.3 * torch.randn((1, v), generator=g, device=DEV))
+        tok = torch.zeros(n, dtype=torch.int32, device=DEV)
+        with KLDStats(n, device=DEV) as st:
+            grad, rows = st.run_grad_packed(base, q, tok, per_row=True)
+        for i in (0, n - 1):
+            lp = torch.log_softmax(base.rows(i, i + 1).unpack()[0].double(), 0)
+            lr = torch.log_softmax(q[i].double(), 0)
+            p, r = lp.exp(), lr.exp()
+            kl, nll = (p * (lp - lr)).sum().item(), -lr[0].item()
+            assert abs(rows["kld"][i].item() - kl) <= 1e-6 + 1e-4 * kl
+            assert abs(rows["nll"][i].item() - nll) <= 1e-6 + 1e-4 * nll
+            off = ((grad[i].double() - (r - p)).abs() - 1e-12) / (p + r)
+            assert off.max().item() <= 4e-6, (step, i, off.max().item())
