@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   } else {
     __syncthreads();
   }
-  if (warp == 0) merge(sh.part, C * kWarps, out.scale, &sh.total);
+  if (warp == 0) merge(sh.part, C * kWarps, out.scale, grow != nullptr, &sh.total);
   __syncthreads();
   // Lowest columns of the row's maxima: the lanes that hold one look through
   // the first chunk in which it appeared; rank 0 collects.

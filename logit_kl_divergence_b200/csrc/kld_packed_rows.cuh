@@ -703,8 +703,9 @@ __device__ __noinline__ State add_later(State s, const RowPtr rp, int64_t V, int
 }
 
 // The parts of a row merged by one warp, in fp64, to the largest frame and
-// the centre of the part that holds the row's maximum.
-__device__ __noinline__ void merge(const Part* part, int parts, float scale, Total* total) {
+// the centre of the part that holds the row's maximum. grad: the gradient's
+// frames too, the base row's on lane 0 and the quant row's on lane 1.
+__device__ __noinline__ void merge(const Part* part, int parts, float scale, bool grad, Total* total) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   float F = kNoFrame, mb = neg_inf(), mq = neg_inf();
   for (int i = lane; i < parts; i += 32) {
@@ -746,26 +747,27 @@ __device__ __noinline__ void merge(const Part* part, int parts, float scale, Tot
   D = warp_sum(D);
   E = warp_sum(E);
   Q = warp_sum(Q);
+  const double q = S + (kLambda * A + C) + Q;
   if (lane == 0) {
-    Total t;
+    Total& t = *total;
     t.S = S + D;
     t.A = A + E;
     t.B = kLambda * A + C + (Q - D);
-    t.q = S + (kLambda * A + C) + Q;
+    t.q = q;
     t.F = F;
     t.K = K;
     t.mb = mb;
     t.mq = mq;
-    t.good = t.S > 0.0 && t.S < 1e300 && fabs(t.A) < 1e300 && t.q > 0.0 && t.q < 1e300 &&
+    t.good = t.S > 0.0 && t.S < 1e300 && fabs(t.A) < 1e300 && q > 0.0 && q < 1e300 &&
              fabsf(F) < 1e6f && fabsf(K) < 1e6f;
-    // sum_j 2^(b_j L) = t.S 2^F, sum_j 2^(q_j L) = t.q 2^(F - K L)
-    const double lb = log2(t.S) + static_cast<double>(F);
-    const double lq = log2(t.q) + static_cast<double>(F) - static_cast<double>(K) * kLog2eD;
-    t.Fb = static_cast<float>(floor(lb));
-    t.Fq = static_cast<float>(floor(lq));
-    t.cb = static_cast<float>(scale * exp2(floor(lb) - lb));
-    t.cq = static_cast<float>(scale * exp2(floor(lq) - lq));
-    *total = t;
+  }
+  if (grad && lane < 2) {
+    // sum_j 2^(b_j L) = (S + D) 2^F, sum_j 2^(q_j L) = q 2^(F - K L)
+    const double at = log2(lane == 0 ? S + D : q) + static_cast<double>(F) -
+                      (lane == 0 ? 0.0 : static_cast<double>(K) * kLog2eD);
+    const float frame = static_cast<float>(floor(at)), c = static_cast<float>(scale * exp2(floor(at) - at));
+    *(lane == 0 ? &total->Fb : &total->Fq) = frame;
+    *(lane == 0 ? &total->cb : &total->cq) = c;
   }
 }
 
