@@ -687,3 +687,36 @@ def test_long_rows_of_equal_values(n, v, value):
             assert abs(rows["nll"][i].item() - nll) <= 1e-6 + 1e-4 * nll
             off = ((grad[i].double() - (r - p)).abs() - 1e-12) / (p + r)
             assert off.max().item() <= 4e-6, (step, i, off.max().item())
+
+
+@pytest.mark.parametrize("quant", ["f32", "packed"])
+@pytest.mark.parametrize("kind", ["rising", "masked", "shifting"])
+def test_long_rows_whose_frames_move(kind, quant):
+    """More than 256 chunks a warp, so that sums move to fp64, with frames and
+    centres that change between the moves, and with masks in every block."""
+    n, v = 380, (1 << 20) + 5
+    g = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn((1, v), generator=g, device=DEV).expand(n, v).contiguous()
+    at = torch.linspace(0.0, 1.0, v, device=DEV)
+    if kind == "rising":
+        x += 80.0 * at
+        q = x + 0.3 * torch.randn((1, v), generator=g, device=DEV)
+    elif kind == "masked":
+        x[:, 3::97] = -math.inf
+        q = x + 0.3 * torch.randn((1, v), generator=g, device=DEV)
+    else:  # the log-ratio drifts by 12 nats, past the polynomial's range
+        x += 20.0 * at
+        q = x - 12.0 * at + 0.3 * torch.randn((1, v), generator=g, device=DEV)
+    base = pack_logits(x)
+    other = pack_logits(q) if quant == "packed" else q
+    tok = torch.full((n,), 1, dtype=torch.int32, device=DEV)
+    with KLDStats(n, device=DEV) as st:
+        grad, rows = st.run_grad_packed(base, other, tok, per_row=True)
+    for i in (0, n - 1):
+        lp = torch.log_softmax(base.rows(i, i + 1).unpack()[0].double(), 0)
+        lr = torch.log_softmax((other.rows(i, i + 1).unpack()[0] if quant == "packed" else q[i]).double(), 0)
+        p, r = lp.exp(), lr.exp()
+        kl, nll = (p * (lp - lr)).nan_to_num(nan=0.0).sum().item(), -lr[1].item()
+        assert abs(rows["kld"][i].item() - kl) <= 1e-6 + 1e-4 * kl
+        assert abs(rows["nll"][i].item() - nll) <= 1e-6 + 1e-4 * nll
+        assert ((grad[i].double() - (r - p)).abs() <= 4e-6 * (p + r) + 1e-12).all()
