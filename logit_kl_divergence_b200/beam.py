@@ -215,8 +215,8 @@ class BeamSearch:
                 raise ValueError("finished must be a bool [groups, beams] tensor")
             if finished.device != self.device or not finished.is_contiguous():
                 raise ValueError("finished must be contiguous and on the handle's device")
-            if eos is None:
-                raise ValueError("finished beams need eos")
+            if eos is None or not 0 <= int(eos) < logits.shape[1]:  # before it is cut to 32 bits
+                raise ValueError("finished beams need eos, a token of the vocabulary")
         s = _on(stream, self.device)
         k = int(k)
         if out is None:
@@ -229,7 +229,7 @@ class BeamSearch:
                     raise ValueError("out must be contiguous float32, int32 and int32 [groups, k] tensors")
         ld = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
         _lib.check(self._lib.kld_beam_select(self._h, logits.data_ptr(), ld, _DTYPES[logits.dtype],
-                                             scores.data_ptr(), _ptr(finished), 0 if eos is None else int(eos),
+                                             scores.data_ptr(), _ptr(finished), 0 if finished is None else int(eos),
                                              groups, beams, logits.shape[1], k, out[0].data_ptr(),
                                              out[1].data_ptr(), out[2].data_ptr(), s), "kld_beam_select")
         return out

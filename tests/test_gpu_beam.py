@@ -475,3 +475,15 @@ def test_parents_and_lengths_between_the_rows_of_a_state():
             beam.reorder([(wide[:, :15], 1)], parents, lens)
         with pytest.raises(ValueError):
             beam.reorder([(wide[:, :14], 1)], parents, lens)
+
+
+def test_eos_outside_the_vocabulary_is_refused():
+    x, s = _rows(4, 100, 1).to(DEV), _scores(2, 2, 1).to(DEV)
+    done = torch.zeros((2, 2), dtype=torch.bool, device=DEV)
+    with BeamSearch(2, 2, device=DEV) as beam:
+        for eos in (None, -1, 100, (1 << 32) + 3, -(1 << 32)):
+            with pytest.raises(ValueError):
+                beam.select(x, s, 2, finished=done, eos=eos)
+        beam.select(x, s, 2, finished=done, eos=99)
+        beam.select(x, s, 2, eos=(1 << 40))  # not looked at
+        assert beam.status() == 0
