@@ -145,9 +145,12 @@ class BeamStates:
     def hold(self, t: torch.Tensor) -> bool:
         """Whether a contiguous tensor shares memory with a state (the gaps
         between a state's runs are not its own)."""
-        a, b = _span(t)
-        return any(a < y and x < b and _holds(s, self.rows, a - x, b - x)
-                   for (x, y), s in zip(self.spans, self.layouts))
+        a = t.data_ptr()
+        b = a + t.numel() * t.element_size()
+        for i, (x, y) in enumerate(self.spans):
+            if a < y and x < b and _holds(self.layouts[i], self.rows, a - x, b - x):
+                return True
+        return False
 
 
 class BeamSearch:
