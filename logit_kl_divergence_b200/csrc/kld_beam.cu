@@ -5,12 +5,14 @@
 //   c(w, j) = s_w + x_wj - lse_w,   lse_w = ln sum_j e^x_wj,
 // and the k largest c over (w, j) leave, best first, ties to the lowest
 // w * V + j. One read of the logits: a row's columns are split over CTAs,
-// each keeping its part of lse (sums of e^(x - m) in fp32 with a thread-level
+// each keeping its part of lse (sums of e^(x - m) with a thread-level
 // frame m that moves only when a value exceeds it by kRaise, fp64 merges, so
-// rows of any magnitude, the type's lowest value included, are summed right)
-// and the entries that can still
-// be among the row's k largest; the last CTA of a group to finish (a ticket)
-// merges lse in fp64, scores the kept entries in fp64 and sorts the best k.
+// rows of any magnitude, the type's lowest value included, are summed right;
+// fp32 exponentials, and their sums over a thread's 16 columns and a warp in
+// fp32, err by 2e-6 in lse at most, as the scores' own fp32 does, and alike in
+// equal rows) and the entries that can still be among the row's k largest; the
+// last CTA of a group to finish (a ticket) merges lse in fp64, scores the kept
+// entries in fp64 and sorts the best k.
 //
 // What can still be among the k largest: any k entries give a bound, since
 // at least k are >= the least of them. The CTA takes its lanes'
@@ -25,7 +27,9 @@
 // Bound by latency for a few rows (4 rows of 32000 bf16: 12 us), by instruction
 // issue and the bounds' barriers for many: 16 instructions an element, one
 // exponential among them, at 55 % of the issue slots. 256 rows of 151936 bf16
-// take 48 us; HBM alone would take 12.
+// take 48 us (fp32 50); HBM alone would take 12. Rows of 151937, most of which
+// have to be shifted, take 53 us at 19 instructions (fp32 65): 48 and 51 when a
+// thread's columns followed the memory's grid, which equal beams cannot have.
 #include <climits>
 #include <type_traits>
 
@@ -446,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
     const int64_t g0 = (part % a.parts) * a.slice;
     const int64_t g1 = g0 + a.slice < V ? g0 + a.slice : V;
     constexpr int64_t kTile = static_cast<int64_t>(kThreads) * kPer;
-    float F = kLowest, S = 0.f, T = neg_inf(), top = neg_inf();  // top: of the lane, so far
+    float F = kLowest, T = neg_inf(), top = neg_inf();  // top: of the lane, so far
+    // In fp64 from one tile to the next: equal terms round alike, so a long
+    // fp32 sum drifts (6e-6 over 64 rows of 2^24 columns of two values).
+    double S = 0.0;
     int renew = 0, tile = 0;  // the tile that renews the bound next
     auto pass = [&](auto shift) {
       Ahead<DT, decltype(shift)::value> next;
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kld_beam_select_kernel(c
     // this CTA's frame and sum
     {
       const float f = warp_max(F);
-      float s = S * ex2((F - f) * kL);
+      float s = static_cast<float>(S) * ex2((F - f) * kL);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == 0) {

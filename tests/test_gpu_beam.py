@@ -487,3 +487,17 @@ def test_eos_outside_the_vocabulary_is_refused():
         beam.select(x, s, 2, finished=done, eos=99)
         beam.select(x, s, 2, eos=(1 << 40))  # not looked at
         assert beam.status() == 0
+
+
+@pytest.mark.parametrize("rows,v", [(2400, 151936), (2400, 1 << 20), (64, 1 << 24)])
+@pytest.mark.parametrize("down", [0.0, 0.6875, 1.90625, 3.09375])
+def test_log_sum_exp_of_long_rows_of_two_values(rows, v, down):
+    """Equal terms round alike, so that the errors of a long fp32 sum add up:
+    the scores of rows that hold one value or two by turns."""
+    x = torch.full((rows, v), 0.5, dtype=torch.bfloat16, device=DEV)
+    x[:, 1::2] -= down
+    with BeamSearch(rows, 1, device=DEV) as beam:
+        s, t, _ = beam.select(x, torch.zeros((rows, 1), device=DEV), 1)
+    assert (t == 0).all()
+    want = math.log(v / 2 * (1.0 + math.exp(-down)))
+    assert (s.double() + want).abs().max().item() <= 2.0 ** -24 * want + 2e-6
