@@ -474,8 +474,8 @@ kld_status_t kld_stats_run_packed(kld_stats_t h, const kld_packed_t* base, const
  * quant_packed is set) read from checkpoints: the same statistic plus
  *   grad[i][j] = scale * (softmax(q_i)_j - softmax(b_i)_j)
  * of the restored values, zero on excluded rows, in one kernel (its second
- * look at a row finds what is still on the chip). grad: caller-owned DEVICE memory, [N, V] of grad_dtype,
- * aligned to its element size; it may be the dense quant rows themselves when
+ * look at a row finds what is still on the chip). grad: caller-owned DEVICE
+ * memory, [N, V] of grad_dtype, aligned to its element size; it may be the dense quant rows themselves when
  * grad_dtype is quant_dtype, and may not overlap the inputs otherwise. A
  * non-finite scale is KLD_ERR_INVALID_ARG.
  */
@@ -499,8 +499,8 @@ typedef struct kld_beam_s* kld_beam_t;
  * up to max_k candidates a group (1 <= max_beams <= 64, 1 <= max_k <= 128).
  * Owns a device workspace of about (2400 + 2 rows) * (16 + 8 c) bytes, rows =
  * max_groups * max_beams and c the power of two from max(128, 8 * max_k) on
- * (2.6 MB for a few rows and max_k <= 16), released by kld_beam_destroy. Bound to one device, not thread-safe; calls
- * whose GPU work overlaps (other streams, graphs replayed at the same time)
+ * (2.6 MB for a few rows and max_k <= 16), released by kld_beam_destroy. Bound
+ * to one device, not thread-safe; calls whose GPU work overlaps (other streams, graphs replayed at the same time)
  * need handles of their own.
  */
 kld_status_t kld_beam_create(kld_beam_t* out, int max_groups, int max_beams, int max_k, int device);
@@ -520,7 +520,9 @@ void kld_beam_destroy(kld_beam_t h);
  * hold -inf, -1, -1. A row with NaN or +inf logits, or without an entry
  * above -inf, offers nothing (KLD_BEAM_NONFINITE), nor does a beam whose
  * score is NaN or +inf (KLD_BEAM_BAD_SCORE). The order is decided by c in
- * fp64. The outputs may not overlap the inputs. beams * V < 2^32,
+ * fp64, its logarithm from fp32 exponentials (within 2e-6, the same in equal
+ * rows); of one row's entries by their logits, where c in fp64 cannot tell
+ * these apart either order may result. The outputs may not overlap the inputs. beams * V < 2^32,
  * 0 <= eos < V when finished is given. Asynchronous on `stream`; allocates
  * nothing, so it may be captured into a graph.
  */

@@ -14,10 +14,11 @@
 // two and rounding to whole numbers below 2^22 are exact in fp32, so a code
 // is decided by no rounded quantity (any fp32 or fp64 evaluation gives the
 // same bits) and every value is an fp32 number. The price against a freely
-// chosen step is a step up to twice as long (1.44 times on average); a block
-// whose entries span few ulps is stored exactly.
+// chosen step is a step up to twice as long (1.44 times on average). Only
+// values on the step's grid are stored exactly; the others are off by at most
+// R / 254 where the block spans R, or 2^-21 max|x| where that is more.
 //   header = base << 9 | (some code is 0) << 8 | (e + 128)
-// The low byte is 2..247 for a block with an unmasked entry, 0 for a fully
+// The low byte is 2..248 for a block with an unmasked entry, 0 for a fully
 // masked one (header 256) and 255 for a block that held NaN, +inf or a
 // magnitude of 2^126 or more (kBadHead; its values read as NaN).
 #pragma once

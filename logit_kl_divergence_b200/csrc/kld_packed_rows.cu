@@ -1,9 +1,9 @@
 // kld_packed_rows.cu -- the statistic and the gradient with packed base rows
 // (mathematics: kld_packed_rows.cuh).
 //
-// Both passes in one launch. A row belongs to one CTA of four
-// warps, or, when there are few rows, to a cluster of 2, 4 or 8 of them, each
-// taking a run of its 512-column chunks. A warp streams its chunks, two at a
+// Both passes in one launch. A row belongs to one CTA of four warps, or, when
+// there are few rows, to a cluster of 2, 4 or 8 of them, each taking a run of
+// its 512-column chunks. A warp streams its chunks, two at a
 // time, through shared-memory slots of its own with cp.async (every global
 // read whole 16-byte vectors in order), 16 columns a lane and chunk in
 // registers. After the sums are merged (every warp leaves its sums in the
@@ -15,10 +15,13 @@
 //
 // Bound by instruction issue: 20 thread instructions an element for the
 // statistic, 13 more for the gradient, at 60-70 % of the issue slots (the
-// rest are the rows' serial ends and the last wave). Five CTAs of 128 threads and 96 registers
-// an SM measured best for the statistic of 8192 x 151936 bf16 (1.04 ms; 64
-// threads 1.18, 256 threads 1.20, 512 threads 1.59 ms); so did two chunks at
-// a time (one: 1.10 ms). Clusters for many rows cost more ends than they save
+// rest are the rows' serial ends and the last wave). The statistic of 8192 x
+// 151936 bf16 takes 1.02 ms, where the row pass over dense bf16 rows, which
+// has no codes to decode, takes 0.91. Five CTAs of 128 threads and 96
+// registers an SM measured best (64 threads 1.18, 256 threads 1.20, 512
+// threads 1.59 ms); the instances spill up to 80 bytes a thread at that, 16-bit
+// quant rows with shifted codes most. So did two chunks at a time (one: 1.10
+// ms). Clusters for many rows cost more ends than they save
 // reads: the gradient of 2048 x 151936 bf16 takes 0.51 ms whole, 0.52 in
 // two, 0.60 in four. A persistent kernel with a producer warp, sixteen consumer
 // warps that run on from row to row and warps that merge behind them was no
